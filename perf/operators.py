@@ -490,8 +490,8 @@ def _own_run(st):
         down = api.GateUpNVFP4(*st["down"], None, None, st["down_scales"])
         return api.nvfp4_expert_layer(st["x"], routing, gateup, down)
     out = api.nvfp4_attention(st["q"], api.NVFP4(*st["k"]), api.NVFP4(*st["v"]),
-                              st["block_table"], st["seq_lens"], case["page"],
-                              window=case["window"])
+                              st["block_table"], st["seq_lens"], case["kv_heads"],
+                              case["page"], window=case["window"])
     return out.out, out.lse
 
 
