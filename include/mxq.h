@@ -71,8 +71,10 @@ extern "C" {
 
 /* Raised whenever an entry point is added or changes (2: the caller-amax
  * export variant, the copy floor, the grouped GEMMs, the grouped
- * weight-gradient pair and the grouped rowwise + transposed quantize). */
-#define MXQ_VERSION 2
+ * weight-gradient pair and the grouped rowwise + transposed quantize; 3: the
+ * layer operators: routing, combine, few-row NVFP4 products, attention over
+ * an NVFP4 cache). */
+#define MXQ_VERSION 3
 
 typedef enum {
     MXQ_OK = 0,
@@ -564,6 +566,235 @@ int mxq_grouped_quantize_dispatch(int fmt, const uint16_t *x, int64_t n_tokens,
  */
 int mxq_copy_floor(const void *src, int64_t src_bytes, void *dst, int64_t dst_bytes,
                    void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Layer operators.  What an expert layer and a rollout's decode step need
+ * around the quantizers and GEMMs above: the router that makes the dispatch's
+ * index maps, the weighted return of expert rows to tokens (both with their
+ * gradients), products of few rows with the exported NVFP4 weights, and
+ * attention over keys and values kept as per-token NVFP4 rows.  Unlike the
+ * quantizers their results are sums, accumulated in fp32 and rounded once at
+ * the end; each call says what it rounds on the way.  The same call on the
+ * same inputs gives the same bytes.  Conventions and errors are those above;
+ * a call that needs scratch memory takes a workspace (16-byte aligned device
+ * memory that belongs to the call until its kernels have run; the size comes
+ * from the call's _workspace function, MXQ_ERR_SIZE if it is smaller).
+ * Infinities are inputs where a call says so; NaN only as stated.
+ */
+typedef enum {
+    MXQ_SCORE_SOFTMAX = 0,     /* scores: softmax over all experts           */
+    MXQ_SCORE_SIGMOID = 1      /* scores: a sigmoid per expert               */
+} mxq_scoring;
+
+typedef enum {
+    MXQ_X_BF16 = 0,            /* activations [rows][K] BF16                 */
+    MXQ_X_F32 = 1,             /* activations [rows][K] fp32                 */
+    MXQ_X_NVFP4 = 2            /* per-token NVFP4: codes, block and FP32 scales */
+} mxq_x_format;
+
+typedef struct {
+    int64_t top_k;             /* experts per token, 1 .. min(n_experts, 64) */
+    int64_t n_groups;          /* expert groups, 1 (none) .. 64, dividing n_experts */
+    int64_t topk_groups;       /* groups kept per token, 1 .. n_groups       */
+    int64_t group_topk;        /* 1 or 2: how many keys sum to a group's score */
+    int scoring;               /* mxq_scoring                                */
+    int renormalize;           /* divide the weights by their sum            */
+    float scale;               /* factor on the weights, finite              */
+} mxq_route_params;
+
+/*
+ * Route tokens to experts.  With x = logits[t], s = softmax(x) or
+ * sigmoid(x) and key = s + bias (bias NULL: 0):
+ *   - with n_groups > 1 the experts form n_groups equal consecutive groups, a
+ *     group scores the sum of its group_topk largest keys (of those it has)
+ *     and the topk_groups best groups stay (ties: the lowest group);
+ *   - the top_k largest keys among the experts that stay are selected, in
+ *     descending order (ties: the lowest expert);
+ *   - weights[t][c] = scale s_c, with renormalize scale s_c / sum of the
+ *     selected s.  The bias moves the selection only, not the weights.
+ * The selection is that of the exact scores: where fp32 cannot decide, it is
+ * decided in 64 bits.  Weights are fp32, within 2^-20 of their value.
+ * An expert whose logit or bias is -inf (or NaN) is never selected; a logit
+ * of +inf counts as the largest finite value.  Where fewer than top_k experts
+ * are left, the other slots get expert -1, weight 0 and no row.
+ *
+ *   logits       [n_tokens][n_experts] BF16 or fp32 (dtype: mxq_out_dtype),
+ *                aligned to its element.
+ *   bias         [n_experts] fp32 or NULL.
+ *   weights      [n_tokens][top_k] fp32;  experts [n_tokens][top_k] int64.
+ *   token_rows   [n_tokens][top_k], row_tokens [n_tokens * top_k],
+ *   seg_offsets  [n_experts + 1], int64: the maps of the expert-sorted layout,
+ *                as mxq_grouped_quantize_dispatch takes them.  Rows are sorted
+ *                by (expert, token); copies with expert -1 have token_rows -1
+ *                and the rows past seg_offsets[n_experts] row_tokens -1.
+ *                All three or none (MXQ_ERR_OFFSETS).
+ *   workspace    mxq_moe_route_workspace(n_tokens, n_experts) bytes; not used
+ *                (may be NULL) without the maps.
+ *   n_experts <= 1024, n_tokens < 2^24, n_tokens * top_k <= 2^30.
+ */
+int mxq_moe_route(int dtype, const void *logits, const float *bias, int64_t n_tokens,
+                  int64_t n_experts, const mxq_route_params *params, float *weights,
+                  int64_t *experts, int64_t *token_rows, int64_t *row_tokens,
+                  int64_t *seg_offsets, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace mxq_moe_route needs (0 for sizes it refuses). */
+int64_t mxq_moe_route_workspace(int64_t n_tokens, int64_t n_experts);
+
+/*
+ * Gradient of the router's weights: d_logits of L given d_weights = dL/dweights,
+ * the selection held fixed (experts as mxq_moe_route returned them; an entry
+ * outside [0, n_experts) contributes nothing).  Scores are recomputed from the
+ * logits in fp32; d_logits has the logits' dtype, every entry written (0 for
+ * an expert whose logit is -inf or NaN).
+ *   top_k <= 64, other sizes as mxq_moe_route.
+ */
+int mxq_moe_route_backward(int dtype, const float *d_weights, const void *logits,
+                           const int64_t *experts, int64_t n_tokens, int64_t n_experts,
+                           int64_t top_k, int scoring, int renormalize, float scale,
+                           void *d_logits, void *stream);
+
+/*
+ * Expert rows back to their tokens:
+ *   out[t] = sum_c weights[t][c] rows[token_rows[t][c]],
+ * accumulated in fp32 in the order of c; entries outside [0, total_rows) are
+ * skipped (a token with none gets zeros).
+ *   rows [total_rows][cols] (dtype) and out [n_tokens][cols] (out_dtype) BF16 or
+ *   fp32, 16-byte aligned; cols % 8 == 0; token_rows, weights [n_tokens][top_k].
+ *   n_tokens < 2^24, top_k <= 64.
+ */
+int mxq_moe_combine(int dtype, const void *rows, int64_t total_rows, const int64_t *token_rows,
+                    const float *weights, int64_t n_tokens, int64_t top_k, int64_t cols,
+                    int out_dtype, void *out, void *stream);
+
+/*
+ * Gradient of the combine: d_rows[token_rows[t][c]] = weights[t][c] d_out[t]
+ * and d_weights[t][c] = sum_k d_out[t][k] rows[token_rows[t][c]][k] (fp32; 0
+ * for a skipped entry).  With seg_offsets ([n_groups + 1], the router's) the
+ * rows from seg_offsets[n_groups] on get zeros; any other row that no entry
+ * names is left unwritten.  With NULL (n_groups ignored) no row is zeroed.
+ * Two entries that name one row leave one of their values in it.
+ *   Sizes and dtypes as mxq_moe_combine.
+ */
+int mxq_moe_combine_backward(int dtype, const void *d_out, const void *rows, int64_t total_rows,
+                             const int64_t *token_rows, const float *weights,
+                             const int64_t *seg_offsets, int64_t n_groups, int64_t n_tokens,
+                             int64_t top_k, int64_t cols, void *d_rows, float *d_weights,
+                             void *stream);
+
+/*
+ * Product of few rows with an NVFP4 weight (a decode step's projections):
+ *   C[m][n] = b_scales[n / rows_per_b_scale] sx[m]
+ *             sum_k x[m][k] dec(b[n][k]) dec(bb[n][k/16]),
+ * sx[m] = 1 for BF16 and fp32 activations, x_scales[m] for NVFP4 ones (whose
+ * x[m][k] is dec(code) dec(block scale)).  Weights and NVFP4 activations enter
+ * the products exactly.  BF16 and fp32 activations are held in FP16 under a
+ * power-of-two scale per row and 256 values: BF16 values within 2^-30 of the
+ * group's largest magnitude are exact, smaller ones off by at most 2^-39 of it;
+ * fp32 values are off by at most 2^-11 relative (or 2^-39 of the largest).
+ * Sums are accumulated in fp32.
+ *   x_fmt: mxq_x_format; x 16-byte aligned ([M][K] BF16 or fp32, or [M][K/2]
+ *   codes), x_block_scales [M][K/16] 4-byte aligned and x_scales [M] for NVFP4
+ *   (MXQ_ERR_OFFSETS if given otherwise, MXQ_ERR_NULL if missing).
+ *   b [N][K/2] 16-byte aligned, b_block_scales [N][K/16] 4-byte aligned,
+ *   b_scales fp32; c [M][N] fp32 or BF16 (out_dtype), aligned to its element.
+ *   K % 64 == 0 (MXQ_ERR_SHAPE), K <= 2^16, M <= 64, N <= 2^24.  For more rows
+ *   quantize them and use mxq_nvfp4_gemm.
+ */
+int mxq_nvfp4_matvec(int x_fmt, const void *x, const uint8_t *x_block_scales,
+                     const float *x_scales, const uint8_t *b, const uint8_t *b_block_scales,
+                     const float *b_scales, int64_t rows_per_b_scale, int64_t M, int64_t N,
+                     int64_t K, int out_dtype, void *c, void *stream);
+
+/*
+ * The same product per expert, on expert-sorted rows: for every row r of
+ * segment e, C[r][n] = b_scales[e] sx[r] sum_k x[r][k] dec(b_e[n][k])
+ * dec(bb_e[n][k/16]) (the down projection of a decode step).
+ *   x, x_fmt, x_block_scales, x_scales as above with total_rows rows; b
+ *   [n_groups][N][K/2], b_block_scales [n_groups][N][K/16], b_scales [n_groups];
+ *   seg_offsets [n_groups + 1], clamped into [0, total_rows] as by
+ *   mxq_nvfp4_grouped_gemm; c [total_rows][N], rows outside every segment are
+ *   not written.
+ *   K, N as above, n_groups <= 2^16, total_rows <= 2^30, and n_groups * ceil(N / 4)
+ *   below 2^24.  Meant for few rows per expert; for many use
+ *   mxq_nvfp4_grouped_gemm.
+ */
+int mxq_nvfp4_expert_matvec(int x_fmt, const void *x, const uint8_t *x_block_scales,
+                            const float *x_scales, const uint8_t *b,
+                            const uint8_t *b_block_scales, const float *b_scales,
+                            const int64_t *seg_offsets, int64_t n_groups, int64_t total_rows,
+                            int64_t N, int64_t K, int out_dtype, void *c, void *stream);
+
+/*
+ * The gate and up projections of the routed experts with the SwiGLU between
+ * them, straight from the unpermuted tokens: for every row r of segment e,
+ * with t = row_tokens[r],
+ *   h[r][n] = silu(g) u,  g = scope_scales[e] sx[t] sum_k x[t][k] gate_e[n][k],
+ *                         u = scope_scales[e] sx[t] sum_k x[t][k] up_e[n][k]
+ * (gate_e, up_e the values dec(code) dec(block scale) of the export under their
+ * shared scale; silu(g) = g / (1 + e^-g) in fp32).
+ *   x as above with n_tokens rows; row_tokens [total_rows], entries clamped
+ *   into [0, n_tokens); gate, up [n_groups][N][K/2] and block scales; scope_scales
+ *   [n_groups]; h [total_rows][N] fp32 or BF16 (out_dtype).  Limits as
+ *   mxq_nvfp4_expert_matvec.
+ */
+int mxq_nvfp4_expert_gateup(int x_fmt, const void *x, const uint8_t *x_block_scales,
+                            const float *x_scales, int64_t n_tokens, const int64_t *row_tokens,
+                            const int64_t *seg_offsets, int64_t n_groups, int64_t total_rows,
+                            const uint8_t *gate, const uint8_t *gate_block_scales,
+                            const uint8_t *up, const uint8_t *up_block_scales,
+                            const float *scope_scales, int64_t N, int64_t K, int out_dtype,
+                            void *h, void *stream);
+
+/* A cache of keys or values: per-token NVFP4 rows of head_dim values, as
+ * mxq_nvfp4_quantize_per_token or the dispatch writes them.  The row of head h
+ * of slot i of page p is (p * n_kv_heads + h) * page_size + i. */
+typedef struct {
+    const uint8_t *codes;         /* [n_pages * n_kv_heads * page_size][head_dim/2] */
+    const uint8_t *block_scales;  /* [..][head_dim/16] E4M3, 8-byte aligned  */
+    const float *scales;          /* [..] FP32, 16-byte aligned              */
+} mxq_nvfp4_cache;
+
+/*
+ * Attention over a paged NVFP4 cache.  Sequence b has n = seq_lens[b] keys, key
+ * t in slot t % page_size of page block_table[b][t / page_size].  Its query
+ * i of q_len stands at position n - q_len + i.  With head h reading key/value
+ * head h / (n_heads / n_kv_heads),
+ *   out[b][i][h] = sum_t p_t V[t],  p = softmax over the keys it sees of
+ *   softmax_scale <q[b][i][h], K[t]>,
+ * where it sees, if causal, the keys up to its position and, if window > 0,
+ * of those only the last `window`; if not causal all n keys.  A query that sees
+ * no key (an empty sequence; a position before the first key) gets zeros and
+ * lse -inf.
+ *   q [n_seqs][q_len][n_heads][head_dim] BF16, out the same, 16-byte aligned.
+ *   lse [n_seqs][q_len][n_heads] fp32 or NULL: the natural log of the softmax's
+ *   sum, with which results over parts of the keys can be joined.
+ *   head_dim 64, 128 or 256; n_heads a multiple of n_kv_heads; page_size a
+ *   multiple of 16 (MXQ_ERR_SHAPE otherwise).
+ *   block_table [n_seqs][max_pages] int64, seq_lens [n_seqs] int64, device data:
+ *   lengths are clamped into [0, max_pages * page_size] and pages into
+ *   [0, n_pages), so malformed ones give meaningless rows, never an access out
+ *   of bounds; entries past a sequence's last page are not read.  Slots past
+ *   the length may hold anything.
+ *   softmax_scale > 0; window >= 0, and 0 if not causal (MXQ_ERR_ARG).
+ *   workspace: mxq_nvfp4_attention_workspace(...) bytes.
+ *   n_seqs * q_len * n_heads <= 2^25, cache rows <= 2^40.
+ * Scores, the running maximum and sum and the output are fp32; q is held in FP16 under
+ * a power-of-two scale per row (as BF16 activations above) and the softmax's
+ * numerators in FP16 (2^-11 relative) under the running maximum of their
+ * products with the values' FP32 scales.
+ */
+int mxq_nvfp4_attention(const uint16_t *q, const mxq_nvfp4_cache *k, const mxq_nvfp4_cache *v,
+                        const int64_t *block_table, const int64_t *seq_lens, int64_t n_seqs,
+                        int64_t q_len, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim,
+                        int64_t n_pages, int64_t page_size, int64_t max_pages,
+                        float softmax_scale, int causal, int64_t window, uint16_t *out,
+                        float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace mxq_nvfp4_attention needs for these sizes, max_keys =
+ * max_pages * page_size (0 for sizes it refuses). */
+int64_t mxq_nvfp4_attention_workspace(int64_t n_seqs, int64_t q_len, int64_t n_heads,
+                                      int64_t n_kv_heads, int64_t head_dim, int64_t max_keys);
 
 /* A static, human-readable message for a status code. */
 const char *mxq_status_string(int status);

@@ -1,7 +1,8 @@
 """MI355X-native bit-exact block-scaled quantizers: MXFP8 (rowwise 1x32 and
 columnwise 32x1 copies, E8M0 scales) and NVFP4 (E2M1 codes, E4M3 block scales,
 per-token or per-scope FP32 scales), with BF16 dequant and grouped (ragged MoE
-segment) variants.  The compute runs in hand-written HIP kernels for gfx950
+segment) variants, and the layer operators around them (routing and combine
+with gradients, few-row NVFP4 products, attention over an NVFP4 cache).  The compute runs in hand-written HIP kernels for gfx950
 behind the C ABI in include/mxq.h (libmxq.so); this package is its ctypes
 binding.  Allocation helpers live in `nvfp4_block_scaled_amax_amd.api`
 (imports torch)."""
@@ -18,4 +19,8 @@ from ._binding import (  # noqa: F401
     mxq_grouped_quantize_dispatch, mxq_copy_floor,
     mxq_mxfp8_quantize_rowcol, mxq_nvfp4_quantize_gateup_pair, mxq_nvfp4_quantize_per_token,
     mxq_nvfp4_quantize_gateup_pair_amax,
-    mxq_quantize_dequant_bf16, mxq_status_string, mxq_version)
+    mxq_quantize_dequant_bf16, mxq_status_string, mxq_version,
+    MXQ_SCORE_SIGMOID, MXQ_SCORE_SOFTMAX, MXQ_X_BF16, MXQ_X_F32, MXQ_X_NVFP4, mxq_moe_combine,
+    mxq_moe_combine_backward, mxq_moe_route, mxq_moe_route_backward, mxq_moe_route_workspace,
+    mxq_nvfp4_attention, mxq_nvfp4_attention_workspace, mxq_nvfp4_cache,
+    mxq_nvfp4_expert_gateup, mxq_nvfp4_expert_matvec, mxq_nvfp4_matvec, mxq_route_params)

@@ -35,6 +35,11 @@ MXQ_FMT_MXFP8_ROWCOL = 3
 MXQ_FMT_NVFP4 = 4
 MXQ_OUT_F32 = 0
 MXQ_OUT_BF16 = 1
+MXQ_SCORE_SOFTMAX = 0
+MXQ_SCORE_SIGMOID = 1
+MXQ_X_BF16 = 0
+MXQ_X_F32 = 1
+MXQ_X_NVFP4 = 2
 
 # Every symbol include/mxq.h declares.
 EXPORTS = (
@@ -57,6 +62,16 @@ EXPORTS = (
     "mxq_grouped_quantize",
     "mxq_grouped_quantize_dispatch",
     "mxq_copy_floor",
+    "mxq_moe_route",
+    "mxq_moe_route_workspace",
+    "mxq_moe_route_backward",
+    "mxq_moe_combine",
+    "mxq_moe_combine_backward",
+    "mxq_nvfp4_matvec",
+    "mxq_nvfp4_expert_matvec",
+    "mxq_nvfp4_expert_gateup",
+    "mxq_nvfp4_attention",
+    "mxq_nvfp4_attention_workspace",
     "mxq_status_string",
     "mxq_version",
 )
@@ -75,6 +90,18 @@ class mxq_grouped_out(ctypes.Structure):
                 ("block_scales", ctypes.c_void_p), ("token_scales", ctypes.c_void_p)]
 
 
+class mxq_route_params(ctypes.Structure):
+    _fields_ = [("top_k", ctypes.c_int64), ("n_groups", ctypes.c_int64),
+                ("topk_groups", ctypes.c_int64), ("group_topk", ctypes.c_int64),
+                ("scoring", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class mxq_nvfp4_cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("block_scales", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -87,7 +114,7 @@ def lib():
         raise RuntimeError(f"libmxq.so is not built ({LIB_PATH}); run "
                            "`python -m nvfp4_block_scaled_amax_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
-    P, I64, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    P, I64, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
     sigs = {
         "mxq_mxfp8_quantize_rowcol": [P, I64, I64, P, P, P, P, P],
         "mxq_nvfp4_quantize_per_token": [P, I64, I64, P, P, P, P],
@@ -109,11 +136,25 @@ def lib():
         "mxq_grouped_quantize_dispatch": [I, P, I64, I64, I64, P, P, I64, P, I64,
                                           ctypes.POINTER(mxq_grouped_out), P],
         "mxq_copy_floor": [P, I64, P, I64, P],
+        "mxq_moe_route": [I, P, P, I64, I64, ctypes.POINTER(mxq_route_params), P, P, P, P, P, P,
+                          I64, P],
+        "mxq_moe_route_workspace": [I64, I64],
+        "mxq_moe_route_backward": [I, P, P, P, I64, I64, I64, I, I, F, P, P],
+        "mxq_moe_combine": [I, P, I64, P, P, I64, I64, I64, I, P, P],
+        "mxq_moe_combine_backward": [I, P, P, I64, P, P, P, I64, I64, I64, I64, P, P, P],
+        "mxq_nvfp4_matvec": [I, P, P, P, P, P, P, I64, I64, I64, I64, I, P, P],
+        "mxq_nvfp4_expert_matvec": [I, P, P, P, P, P, P, P, I64, I64, I64, I64, I, P, P],
+        "mxq_nvfp4_expert_gateup": [I, P, P, P, I64, P, P, I64, I64, P, P, P, P, P, I64, I64, I,
+                                    P, P],
+        "mxq_nvfp4_attention": [P, ctypes.POINTER(mxq_nvfp4_cache),
+                                ctypes.POINTER(mxq_nvfp4_cache), P, P, I64, I64, I64, I64, I64,
+                                I64, I64, I64, F, I, I64, P, P, P, I64, P],
+        "mxq_nvfp4_attention_workspace": [I64] * 6,
     }
     for name, args in sigs.items():
         f = getattr(L, name)
         f.argtypes = args
-        f.restype = I
+        f.restype = I64 if name.endswith("_workspace") else I
     L.mxq_status_string.argtypes = [I]
     L.mxq_status_string.restype = ctypes.c_char_p
     L.mxq_version.argtypes = []
@@ -319,3 +360,97 @@ def mxq_grouped_quantize_dispatch(fmt, x, n_tokens, cols, top_k, token_rows, row
 def mxq_copy_floor(src, src_bytes, dst, dst_bytes, stream=None):
     _check(lib().mxq_copy_floor(_ptr(src), src_bytes, _ptr(dst), dst_bytes, _stream(stream)),
            "mxq_copy_floor")
+
+
+def mxq_moe_route_workspace(n_tokens, n_experts) -> int:
+    return lib().mxq_moe_route_workspace(n_tokens, n_experts)
+
+
+def mxq_moe_route(dtype, logits, bias, n_tokens, n_experts, params, weights, experts, token_rows,
+                  row_tokens, seg_offsets, workspace, workspace_bytes, stream=None):
+    """`params`: an mxq_route_params, or a dict with its field names."""
+    if not isinstance(params, mxq_route_params):
+        params = mxq_route_params(**params)
+    _check(lib().mxq_moe_route(dtype, _ptr(logits), _ptr(bias), n_tokens, n_experts,
+                               ctypes.byref(params), _ptr(weights), _ptr(experts),
+                               _ptr(token_rows), _ptr(row_tokens), _ptr(seg_offsets),
+                               _ptr(workspace), workspace_bytes, _stream(stream)),
+           "mxq_moe_route")
+
+
+def mxq_moe_route_backward(dtype, d_weights, logits, experts, n_tokens, n_experts, top_k,
+                           scoring, renormalize, scale, d_logits, stream=None):
+    _check(lib().mxq_moe_route_backward(dtype, _ptr(d_weights), _ptr(logits), _ptr(experts),
+                                        n_tokens, n_experts, top_k, scoring, int(renormalize),
+                                        scale, _ptr(d_logits), _stream(stream)),
+           "mxq_moe_route_backward")
+
+
+def mxq_moe_combine(dtype, rows, total_rows, token_rows, weights, n_tokens, top_k, cols,
+                    out_dtype, out, stream=None):
+    _check(lib().mxq_moe_combine(dtype, _ptr(rows), total_rows, _ptr(token_rows), _ptr(weights),
+                                 n_tokens, top_k, cols, out_dtype, _ptr(out), _stream(stream)),
+           "mxq_moe_combine")
+
+
+def mxq_moe_combine_backward(dtype, d_out, rows, total_rows, token_rows, weights, seg_offsets,
+                             n_groups, n_tokens, top_k, cols, d_rows, d_weights, stream=None):
+    _check(lib().mxq_moe_combine_backward(dtype, _ptr(d_out), _ptr(rows), total_rows,
+                                          _ptr(token_rows), _ptr(weights), _ptr(seg_offsets),
+                                          n_groups, n_tokens, top_k, cols, _ptr(d_rows),
+                                          _ptr(d_weights), _stream(stream)),
+           "mxq_moe_combine_backward")
+
+
+def mxq_nvfp4_matvec(x_fmt, x, x_block_scales, x_scales, b, b_block_scales, b_scales,
+                     rows_per_b_scale, M, N, K, out_dtype, c, stream=None):
+    _check(lib().mxq_nvfp4_matvec(x_fmt, _ptr(x), _ptr(x_block_scales), _ptr(x_scales), _ptr(b),
+                                  _ptr(b_block_scales), _ptr(b_scales), rows_per_b_scale, M, N,
+                                  K, out_dtype, _ptr(c), _stream(stream)),
+           "mxq_nvfp4_matvec")
+
+
+def mxq_nvfp4_expert_matvec(x_fmt, x, x_block_scales, x_scales, b, b_block_scales, b_scales,
+                            seg_offsets, n_groups, total_rows, N, K, out_dtype, c, stream=None):
+    _check(lib().mxq_nvfp4_expert_matvec(x_fmt, _ptr(x), _ptr(x_block_scales), _ptr(x_scales),
+                                         _ptr(b), _ptr(b_block_scales), _ptr(b_scales),
+                                         _ptr(seg_offsets), n_groups, total_rows, N, K,
+                                         out_dtype, _ptr(c), _stream(stream)),
+           "mxq_nvfp4_expert_matvec")
+
+
+def mxq_nvfp4_expert_gateup(x_fmt, x, x_block_scales, x_scales, n_tokens, row_tokens,
+                            seg_offsets, n_groups, total_rows, gate, gate_block_scales, up,
+                            up_block_scales, scope_scales, N, K, out_dtype, h, stream=None):
+    _check(lib().mxq_nvfp4_expert_gateup(x_fmt, _ptr(x), _ptr(x_block_scales), _ptr(x_scales),
+                                         n_tokens, _ptr(row_tokens), _ptr(seg_offsets),
+                                         n_groups, total_rows, _ptr(gate),
+                                         _ptr(gate_block_scales), _ptr(up),
+                                         _ptr(up_block_scales), _ptr(scope_scales), N, K,
+                                         out_dtype, _ptr(h), _stream(stream)),
+           "mxq_nvfp4_expert_gateup")
+
+
+def mxq_nvfp4_attention_workspace(n_seqs, q_len, n_heads, n_kv_heads, head_dim, max_keys) -> int:
+    return lib().mxq_nvfp4_attention_workspace(n_seqs, q_len, n_heads, n_kv_heads, head_dim,
+                                               max_keys)
+
+
+def _cache(c):
+    if c is None or isinstance(c, mxq_nvfp4_cache):
+        return c
+    return mxq_nvfp4_cache(*(_ptr(a) for a in c))
+
+
+def mxq_nvfp4_attention(q, k, v, block_table, seq_lens, n_seqs, q_len, n_heads, n_kv_heads,
+                        head_dim, n_pages, page_size, max_pages, softmax_scale, causal, window,
+                        out, lse, workspace, workspace_bytes, stream=None):
+    """`k`, `v`: an mxq_nvfp4_cache, or (codes, block_scales, scales)."""
+    k, v = _cache(k), _cache(v)
+    _check(lib().mxq_nvfp4_attention(_ptr(q), None if k is None else ctypes.byref(k),
+                                     None if v is None else ctypes.byref(v), _ptr(block_table),
+                                     _ptr(seq_lens), n_seqs, q_len, n_heads, n_kv_heads,
+                                     head_dim, n_pages, page_size, max_pages, softmax_scale,
+                                     int(causal), window, _ptr(out), _ptr(lse), _ptr(workspace),
+                                     workspace_bytes, _stream(stream)),
+           "mxq_nvfp4_attention")

@@ -382,3 +382,265 @@ def dispatch_quantize_nvfp4(tokens, token_rows, total_rows, stream=None) -> NVFP
                                     {"codes": res.codes, "block_scales": res.block_scales,
                                      "token_scales": res.fp32_scales}, stream)
     return res
+
+
+# ---------------------------------------------------------------------------
+# Layer operators
+# ---------------------------------------------------------------------------
+
+def _dtype_code(t: torch.Tensor, what: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return B.MXQ_OUT_BF16
+    if t.dtype == torch.float32:
+        return B.MXQ_OUT_F32
+    raise TypeError(f"{what} must be BF16 or FP32, got {t.dtype}")
+
+
+def _out_code(dtype) -> int:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    return B.MXQ_OUT_BF16 if dtype == torch.bfloat16 else B.MXQ_OUT_F32
+
+
+def _arg(t, what: str, dtype, shape=None):
+    """A tensor argument of the given dtype and shape (None: any size), contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or
+                              any(w is not None and n != w for n, w in zip(t.shape, shape))):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t
+
+
+def _workspace(nbytes: int, like):
+    return _empty((nbytes,), torch.uint8, like) if nbytes else None
+
+
+class Routing(NamedTuple):
+    weights: torch.Tensor                    # [T][top_k] FP32
+    experts: torch.Tensor                    # [T][top_k] int64, -1: none left
+    token_rows: Optional[torch.Tensor]       # [T][top_k] int64, -1: no row
+    row_tokens: Optional[torch.Tensor]       # [T * top_k] int64
+    seg_offsets: Optional[torch.Tensor]      # [n_experts + 1] int64
+
+
+def moe_route(logits, top_k: int, bias=None, scoring: int = B.MXQ_SCORE_SOFTMAX,
+              n_expert_groups: int = 1, topk_groups: int = 1, group_topk: int = 1,
+              renormalize: bool = True, scale: float = 1.0, maps: bool = True,
+              stream=None) -> Routing:
+    """Experts, weights and the dispatch's index maps of each token from its
+    router logits [T][n_experts] (BF16 or FP32); bias [n_experts] FP32 moves
+    the selection only.  maps=False leaves the maps out (None)."""
+    code = _dtype_code(logits, "logits")
+    T, E = _arg(logits, "logits", logits.dtype, (None, None)).shape
+    if bias is not None:
+        _arg(bias, "bias", torch.float32, (E,))
+    w = _empty((T, top_k), torch.float32, logits)
+    e = _empty((T, top_k), torch.int64, logits)
+    tr = rt = seg = ws = None
+    nbytes = 0
+    if maps:
+        tr = _empty((T, top_k), torch.int64, logits)
+        rt = _empty((T * top_k,), torch.int64, logits)
+        seg = _empty((E + 1,), torch.int64, logits)
+        nbytes = B.mxq_moe_route_workspace(T, E)
+        ws = _workspace(nbytes, logits)
+    params = B.mxq_route_params(top_k, n_expert_groups, topk_groups, group_topk, scoring,
+                                int(renormalize), scale)
+    B.mxq_moe_route(code, logits, bias, T, E, params, w, e, tr, rt, seg, ws, nbytes, stream)
+    return Routing(w, e, tr, rt, seg)
+
+
+def moe_route_backward(d_weights, logits, experts, scoring: int = B.MXQ_SCORE_SOFTMAX,
+                       renormalize: bool = True, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """d_logits of the router's weights, the selection held fixed."""
+    code = _dtype_code(logits, "logits")
+    T, E = _arg(logits, "logits", logits.dtype, (None, None)).shape
+    k = _arg(experts, "experts", torch.int64, (T, None)).shape[1]
+    _arg(d_weights, "d_weights", torch.float32, (T, k))
+    d = torch.empty_like(logits)
+    B.mxq_moe_route_backward(code, d_weights, logits, experts, T, E, k, scoring, renormalize,
+                             scale, d, stream)
+    return d
+
+
+def moe_combine(rows, token_rows, weights, out_dtype=None, stream=None) -> torch.Tensor:
+    """out[t] = sum_c weights[t][c] rows[token_rows[t][c]], [T][cols], in
+    out_dtype (by default the dtype of rows, BF16 or FP32)."""
+    code = _dtype_code(rows, "rows")
+    R, cols = _arg(rows, "rows", rows.dtype, (None, None)).shape
+    T, k = _arg(token_rows, "token_rows", torch.int64, (None, None)).shape
+    _arg(weights, "weights", torch.float32, (T, k))
+    out_dtype = rows.dtype if out_dtype is None else out_dtype
+    out_code = _out_code(out_dtype)
+    out = _empty((T, cols), out_dtype, rows)
+    B.mxq_moe_combine(code, rows, R, token_rows, weights, T, k, cols, out_code, out, stream)
+    return out
+
+
+def moe_combine_backward(d_out, rows, token_rows, weights, seg_offsets=None, stream=None):
+    """(d_rows, d_weights) of moe_combine.  With the router's seg_offsets the
+    rows past the last segment get zeros; other rows that no entry of
+    token_rows names are left unwritten."""
+    code = _dtype_code(rows, "rows")
+    R, cols = _arg(rows, "rows", rows.dtype, (None, None)).shape
+    T, k = _arg(token_rows, "token_rows", torch.int64, (None, None)).shape
+    _arg(weights, "weights", torch.float32, (T, k))
+    _arg(d_out, "d_out", rows.dtype, (T, cols))
+    G = 0
+    if seg_offsets is not None:
+        G = _arg(seg_offsets, "seg_offsets", torch.int64, (None,)).numel() - 1
+    d_rows = torch.empty_like(rows)
+    d_w = _empty((T, k), torch.float32, rows)
+    B.mxq_moe_combine_backward(code, d_out, rows, R, token_rows, weights, seg_offsets, G, T, k,
+                               cols, d_rows, d_w, stream)
+    return d_rows, d_w
+
+
+def _activations(x):
+    """(format, codes or values, block scales, FP32 scales, rows, K) of an
+    activation operand: a BF16 or FP32 tensor [rows][K] or an NVFP4 tuple."""
+    if isinstance(x, tuple):
+        x = NVFP4(*x)
+        rows, half = _arg(x.codes, "x codes", torch.uint8, (None, None)).shape
+        _arg(x.block_scales, "x block scales", torch.uint8, (rows, half // 8))
+        _arg(x.fp32_scales, "x FP32 scales", torch.float32, (rows,))
+        return B.MXQ_X_NVFP4, x.codes, x.block_scales, x.fp32_scales, rows, 2 * half
+    code = _dtype_code(x, "x")
+    rows, K = _arg(x, "x", x.dtype, (None, None)).shape
+    return (B.MXQ_X_BF16 if code == B.MXQ_OUT_BF16 else B.MXQ_X_F32), x, None, None, rows, K
+
+
+def _nvfp4_weight(codes, block_scales, lead, K, what):
+    """N of a weight [*lead][N][K] in NVFP4."""
+    shape = (*lead, None, K // 2)
+    N = _arg(codes, f"{what} codes", torch.uint8, shape).shape[-2]
+    _arg(block_scales, f"{what} block scales", torch.uint8, (*lead, N, K // 16))
+    return N
+
+
+def nvfp4_matvec(x, b_codes, b_block_scales, b_scales, rows_per_b_scale: Optional[int] = None,
+                 out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """C = x W^T for few rows x (at most 64): BF16 or FP32 [M][K], or an NVFP4
+    tuple of per-token rows; W [N][K] in NVFP4 with one FP32 scale per
+    rows_per_b_scale rows (by default one for all).  Returns C [M][N]."""
+    fmt, xv, xbs, xs, M, K = _activations(x)
+    N = _nvfp4_weight(b_codes, b_block_scales, (), K, "b")
+    rpb = N if rows_per_b_scale is None else rows_per_b_scale
+    if rpb > 0:
+        _arg(b_scales, "b scales", torch.float32, (-(-N // rpb),))
+    code = _out_code(out_dtype)
+    c = _empty((M, N), out_dtype, xv)
+    B.mxq_nvfp4_matvec(fmt, xv, xbs, xs, b_codes, b_block_scales, b_scales, rpb, M, N, K, code,
+                       c, stream)
+    return c
+
+
+def nvfp4_expert_matvec(x, b_codes, b_block_scales, b_scales, seg_offsets,
+                        out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """C[r] = x[r] W_e^T for the rows r of each segment e of seg_offsets: x
+    [R][K] expert-sorted (as nvfp4_matvec), W [G][N][K] in NVFP4 with one FP32
+    scale per expert.  Rows outside every segment are left unwritten."""
+    fmt, xv, xbs, xs, R, K = _activations(x)
+    G = _arg(seg_offsets, "seg_offsets", torch.int64, (None,)).numel() - 1
+    N = _nvfp4_weight(b_codes, b_block_scales, (G,), K, "b")
+    _arg(b_scales, "b scales", torch.float32, (G,))
+    code = _out_code(out_dtype)
+    c = _empty((R, N), out_dtype, xv)
+    B.mxq_nvfp4_expert_matvec(fmt, xv, xbs, xs, b_codes, b_block_scales, b_scales, seg_offsets, G,
+                              R, N, K, code, c, stream)
+    return c
+
+
+def nvfp4_expert_gateup(x, gateup: GateUpNVFP4, row_tokens, seg_offsets,
+                        out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """h[r] = silu(x[t] gate_e^T) * (x[t] up_e^T), t = row_tokens[r], for the
+    rows r of each segment e: x [T][K] unpermuted tokens (as nvfp4_matvec),
+    gateup the experts' exported pair.  Returns h [R][N]."""
+    fmt, xv, xbs, xs, T, K = _activations(x)
+    G = _arg(seg_offsets, "seg_offsets", torch.int64, (None,)).numel() - 1
+    R = _arg(row_tokens, "row_tokens", torch.int64, (None,)).numel()
+    if gateup.up_codes is None:
+        raise ValueError("gateup must hold the up projection")
+    N = _nvfp4_weight(gateup.gate_codes, gateup.gate_block_scales, (G,), K, "gate")
+    if _nvfp4_weight(gateup.up_codes, gateup.up_block_scales, (G,), K, "up") != N:
+        raise ValueError("gate and up must have the same shape")
+    _arg(gateup.scope_scales, "scope scales", torch.float32, (G,))
+    code = _out_code(out_dtype)
+    h = _empty((R, N), out_dtype, xv)
+    B.mxq_nvfp4_expert_gateup(fmt, xv, xbs, xs, T, row_tokens, seg_offsets, G, R,
+                              gateup.gate_codes, gateup.gate_block_scales, gateup.up_codes,
+                              gateup.up_block_scales, gateup.scope_scales, N, K, code, h, stream)
+    return h
+
+
+def nvfp4_expert_layer(x, routing: Routing, gateup: GateUpNVFP4, down: GateUpNVFP4,
+                       stream=None) -> torch.Tensor:
+    """The expert layer of a decode step: the routed experts' gate/up with
+    SwiGLU, down, and the weighted return to the tokens.  x [T][K] BF16, FP32
+    or NVFP4; gateup and down as nvfp4_quantize_gateup_pair exports them (down
+    with up=None).  Intermediates are FP32; returns BF16 [T][N]."""
+    h = nvfp4_expert_gateup(x, gateup, routing.row_tokens, routing.seg_offsets, stream=stream)
+    y = nvfp4_expert_matvec(h, down.gate_codes, down.gate_block_scales, down.scope_scales,
+                            routing.seg_offsets, stream=stream)
+    return moe_combine(y, routing.token_rows, routing.weights, torch.bfloat16, stream)
+
+
+class Attention(NamedTuple):
+    out: torch.Tensor          # [n_seqs][q_len][n_heads][head_dim] BF16
+    lse: torch.Tensor          # [n_seqs][q_len][n_heads] FP32
+
+
+def nvfp4_cache_rows(pages, slots, n_kv_heads: int, page_size: int) -> torch.Tensor:
+    """Rows of an NVFP4 cache, [T][n_kv_heads] int64, of tokens at slot slots[t] of
+    page pages[t]: the token_rows under which dispatch_quantize_nvfp4's
+    library call writes their keys (or values) into the cache."""
+    heads = torch.arange(n_kv_heads, device=pages.device)
+    return (pages[:, None] * n_kv_heads + heads) * page_size + slots[:, None]
+
+
+def nvfp4_cache_append(x, rows, cache: NVFP4, stream=None) -> None:
+    """Quantize keys or values x [T][n_kv_heads][head_dim] (BF16) into the rows
+    [T][n_kv_heads] of the cache; a row of -1 is dropped."""
+    x = _bf16_bits(x)
+    T, H, D = x.shape
+    _arg(rows, "rows", torch.int64, (T, H))
+    n = _arg(cache.codes, "cache codes", torch.uint8, (None, D // 2)).shape[0]
+    _arg(cache.block_scales, "cache block scales", torch.uint8, (n, D // 16))
+    _arg(cache.fp32_scales, "cache FP32 scales", torch.float32, (n,))
+    B.mxq_grouped_quantize_dispatch(B.MXQ_FMT_NVFP4, x, T * H, D, 1, rows, None, n, None, 0,
+                                    {"codes": cache.codes, "block_scales": cache.block_scales,
+                                     "token_scales": cache.fp32_scales}, stream)
+
+
+def nvfp4_attention(q, k: NVFP4, v: NVFP4, block_table, seq_lens, n_kv_heads: int,
+                    page_size: int, softmax_scale: Optional[float] = None, causal: bool = True,
+                    window: int = 0, stream=None) -> Attention:
+    """Attention of q [n_seqs][q_len][n_heads][head_dim] (BF16) over a paged
+    cache of NVFP4 keys and values (rows [n_pages * n_kv_heads * page_size], see
+    nvfp4_cache_rows); block_table [n_seqs][max_pages] and seq_lens [n_seqs]
+    int64.  The queries are the last q_len positions of their sequence;
+    softmax_scale is 1/sqrt(head_dim) by default."""
+    _arg(q, "q", torch.bfloat16, (None, None, None, None))
+    n_seqs, q_len, n_heads, D = q.shape
+    n_rows = _arg(k.codes, "k codes", torch.uint8, (None, D // 2)).shape[0]
+    for name, c in (("k", k), ("v", v)):
+        _arg(c.codes, f"{name} codes", torch.uint8, (n_rows, D // 2))
+        _arg(c.block_scales, f"{name} block scales", torch.uint8, (n_rows, D // 16))
+        _arg(c.fp32_scales, f"{name} FP32 scales", torch.float32, (n_rows,))
+    max_pages = _arg(block_table, "block_table", torch.int64, (n_seqs, None)).shape[1]
+    _arg(seq_lens, "seq_lens", torch.int64, (n_seqs,))
+    per_page = n_kv_heads * page_size
+    if per_page < 1 or n_rows % per_page != 0:
+        raise ValueError("the cache must hold n_pages * n_kv_heads * page_size rows")
+    scale = D ** -0.5 if softmax_scale is None else softmax_scale
+    out = torch.empty_like(q)
+    lse = _empty((n_seqs, q_len, n_heads), torch.float32, q)
+    nbytes = B.mxq_nvfp4_attention_workspace(n_seqs, q_len, n_heads, n_kv_heads, D,
+                                             max_pages * page_size)
+    B.mxq_nvfp4_attention(q, k, v, block_table, seq_lens, n_seqs, q_len, n_heads, n_kv_heads, D,
+                          n_rows // per_page, page_size, max_pages, scale, causal, window, out,
+                          lse, _workspace(nbytes, q), nbytes, stream)
+    return Attention(out, lse)

@@ -6,8 +6,10 @@
 
 #include <stddef.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "mxq_launch.h"
+#include "mxq_layer.h"
 
 namespace {
 
@@ -27,6 +29,13 @@ constexpr int64_t MAX_GRID_ROWS = mxq::MAX_TOKEN_ROWS;   // per-token NVFP4: one
 constexpr int64_t MAX_BLOCKS = 0xFFFFFFFF;        // 16-element blocks indexed in 32 bits
 constexpr int64_t MAX_MXFP8_COLS = (int64_t)1 << 26;  // 32-row tile offsets fit 32 bits
 constexpr int64_t MAX_COPY_FLOOR_BYTES = (int64_t)1 << 35;
+// Layer operators: one workgroup of at most 256 threads per token, and the
+// sizes the few-row products and the attention index with 32 bits.
+constexpr int64_t MAX_LAYER_TOKENS = (int64_t)1 << 24;
+constexpr int64_t MAX_MATVEC_ROWS = 64, MAX_MATVEC_N = (int64_t)1 << 24;
+constexpr int64_t MAX_MATVEC_K = (int64_t)1 << 16, MAX_MATVEC_GROUPS = (int64_t)1 << 16;
+constexpr int64_t MAX_ATTN_ROWS = (int64_t)1 << 25, MAX_ATTN_KEYS = (int64_t)1 << 31;
+constexpr int64_t MAX_CACHE_ROWS = (int64_t)1 << 40;
 
 bool size_ok(int64_t a, int64_t b)
 {
@@ -834,6 +843,400 @@ int mxq_copy_floor(const void *src, int64_t src_bytes, void *dst, int64_t dst_by
     if (st != MXQ_OK)
         return st;
     return launched(mxq::launch_copy_floor(src, src_bytes, dst, dst_bytes, (hipStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// Layer operators
+// ---------------------------------------------------------------------------
+
+static bool route_sizes_ok(int64_t n_tokens, int64_t n_experts)
+{
+    return n_tokens > 0 && n_experts > 0 && n_tokens < MAX_LAYER_TOKENS &&
+           n_experts <= mxq::MAX_EXPERTS;
+}
+
+static bool dtype_ok(int dtype)
+{
+    return dtype == MXQ_OUT_F32 || dtype == MXQ_OUT_BF16;
+}
+
+// By bits, hidden from the compiler as bits of a float: under -fno-honor-nans
+// it may otherwise merge the test with a comparison and lose the NaN.
+static bool finite_f32(float f)
+{
+    uint32_t u;
+    memcpy(&u, &f, sizeof u);
+    __asm__("" : "+r"(u));
+    return (u & 0x7F800000u) != 0x7F800000u;
+}
+
+int64_t mxq_moe_route_workspace(int64_t n_tokens, int64_t n_experts)
+{
+    return route_sizes_ok(n_tokens, n_experts) ? mxq::moe_route_workspace(n_tokens, n_experts)
+                                               : 0;
+}
+
+int mxq_moe_route(int dtype, const void *logits, const float *bias, int64_t n_tokens,
+                  int64_t n_experts, const mxq_route_params *params, float *weights,
+                  int64_t *experts, int64_t *token_rows, int64_t *row_tokens,
+                  int64_t *seg_offsets, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!dtype_ok(dtype))
+        return MXQ_ERR_ARG;
+    if (!logits || !params || !weights || !experts)
+        return MXQ_ERR_NULL;
+    const mxq_route_params p = *params;
+    if ((p.scoring != MXQ_SCORE_SOFTMAX && p.scoring != MXQ_SCORE_SIGMOID) ||
+        (p.group_topk != 1 && p.group_topk != 2) || !finite_f32(p.scale))
+        return MXQ_ERR_ARG;
+    const bool maps = token_rows != nullptr;
+    if ((row_tokens != nullptr) != maps || (seg_offsets != nullptr) != maps)
+        return MXQ_ERR_OFFSETS;
+    if (!route_sizes_ok(n_tokens, n_experts) || p.top_k < 1 || p.top_k > n_experts ||
+        p.top_k > mxq::MAX_TOP_K || n_tokens > mxq::MAX_COPIES / p.top_k || p.n_groups < 1 ||
+        p.n_groups > 64 || p.topk_groups < 1 || p.topk_groups > p.n_groups)
+        return MXQ_ERR_SIZE;
+    if (n_experts % p.n_groups != 0)
+        return MXQ_ERR_SHAPE;
+    const int64_t need = maps ? mxq::moe_route_workspace(n_tokens, n_experts) : 0;
+    if (need > 0 && !workspace)
+        return MXQ_ERR_NULL;
+    if (workspace_bytes < need)
+        return MXQ_ERR_SIZE;
+    const int esz = dtype == MXQ_OUT_F32 ? 4 : 2;
+    const int64_t copies = n_tokens * p.top_k;
+    Buf b[8];
+    int k = 0;
+    b[k++] = {logits, esz * n_tokens * n_experts, esz, false};
+    b[k++] = {weights, 4 * copies, 4, true};
+    b[k++] = {experts, 8 * copies, 8, true};
+    if (bias)
+        b[k++] = {bias, 4 * n_experts, 4, false};
+    if (maps) {
+        b[k++] = {token_rows, 8 * copies, 8, true};
+        b[k++] = {row_tokens, 8 * copies, 8, true};
+        b[k++] = {seg_offsets, 8 * (n_experts + 1), 8, true};
+        b[k++] = {workspace, need, 16, true};
+    }
+    const int st = check_bufs(b, k);
+    if (st != MXQ_OK)
+        return st;
+    return launched(mxq::launch_moe_route(dtype == MXQ_OUT_BF16, logits, bias, n_tokens,
+                                          n_experts, p, weights, experts, token_rows, row_tokens,
+                                          seg_offsets, workspace, (hipStream_t)stream));
+}
+
+int mxq_moe_route_backward(int dtype, const float *d_weights, const void *logits,
+                           const int64_t *experts, int64_t n_tokens, int64_t n_experts,
+                           int64_t top_k, int scoring, int renormalize, float scale,
+                           void *d_logits, void *stream)
+{
+    if (!dtype_ok(dtype) || (scoring != MXQ_SCORE_SOFTMAX && scoring != MXQ_SCORE_SIGMOID) ||
+        !finite_f32(scale))
+        return MXQ_ERR_ARG;
+    if (!d_weights || !logits || !experts || !d_logits)
+        return MXQ_ERR_NULL;
+    if (!route_sizes_ok(n_tokens, n_experts) || top_k < 1 || top_k > mxq::MAX_TOP_K ||
+        n_tokens > mxq::MAX_COPIES / top_k)
+        return MXQ_ERR_SIZE;
+    const int esz = dtype == MXQ_OUT_F32 ? 4 : 2;
+    const Buf b[4] = {{d_weights, 4 * n_tokens * top_k, 4, false},
+                      {logits, esz * n_tokens * n_experts, esz, false},
+                      {experts, 8 * n_tokens * top_k, 8, false},
+                      {d_logits, esz * n_tokens * n_experts, esz, true}};
+    const int st = check_bufs(b, 4);
+    if (st != MXQ_OK)
+        return st;
+    return launched(mxq::launch_moe_route_backward(
+        dtype == MXQ_OUT_BF16, d_weights, logits, experts, n_tokens, n_experts, top_k,
+        scoring == MXQ_SCORE_SIGMOID, renormalize != 0, scale, d_logits, (hipStream_t)stream));
+}
+
+static int combine_sizes(int64_t total_rows, int64_t n_tokens, int64_t top_k, int64_t cols)
+{
+    if (!size_ok(total_rows, 4 * cols) || cols > MAX_ELEMS / 4 || n_tokens < 1 ||
+        n_tokens >= MAX_LAYER_TOKENS || top_k < 1 || top_k > mxq::MAX_TOP_K ||
+        !size_ok(n_tokens, 4 * cols))
+        return MXQ_ERR_SIZE;
+    return cols % 8 != 0 ? MXQ_ERR_SHAPE : MXQ_OK;
+}
+
+int mxq_moe_combine(int dtype, const void *rows, int64_t total_rows, const int64_t *token_rows,
+                    const float *weights, int64_t n_tokens, int64_t top_k, int64_t cols,
+                    int out_dtype, void *out, void *stream)
+{
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype))
+        return MXQ_ERR_ARG;
+    if (!rows || !token_rows || !weights || !out)
+        return MXQ_ERR_NULL;
+    int st = combine_sizes(total_rows, n_tokens, top_k, cols);
+    if (st != MXQ_OK)
+        return st;
+    const int esz = dtype == MXQ_OUT_F32 ? 4 : 2;
+    const Buf b[4] = {{rows, esz * total_rows * cols, 16, false},
+                      {token_rows, 8 * n_tokens * top_k, 8, false},
+                      {weights, 4 * n_tokens * top_k, 4, false},
+                      {out, (out_dtype == MXQ_OUT_F32 ? 4 : 2) * n_tokens * cols, 16, true}};
+    st = check_bufs(b, 4);
+    if (st != MXQ_OK)
+        return st;
+    return launched(mxq::launch_moe_combine(dtype == MXQ_OUT_BF16, rows, total_rows, token_rows,
+                                            weights, n_tokens, top_k, cols,
+                                            out_dtype == MXQ_OUT_BF16, out,
+                                            (hipStream_t)stream));
+}
+
+int mxq_moe_combine_backward(int dtype, const void *d_out, const void *rows, int64_t total_rows,
+                             const int64_t *token_rows, const float *weights,
+                             const int64_t *seg_offsets, int64_t n_groups, int64_t n_tokens,
+                             int64_t top_k, int64_t cols, void *d_rows, float *d_weights,
+                             void *stream)
+{
+    if (!dtype_ok(dtype))
+        return MXQ_ERR_ARG;
+    if (!d_out || !rows || !token_rows || !weights || !d_rows || !d_weights)
+        return MXQ_ERR_NULL;
+    if (seg_offsets && (n_groups < 1 || n_groups > MAX_ELEMS / 8 - 1))
+        return MXQ_ERR_SIZE;
+    int st = combine_sizes(total_rows, n_tokens, top_k, cols);
+    if (st != MXQ_OK)
+        return st;
+    const int esz = dtype == MXQ_OUT_F32 ? 4 : 2;
+    Buf b[7];
+    int k = 0;
+    b[k++] = {d_out, esz * n_tokens * cols, 16, false};
+    b[k++] = {rows, esz * total_rows * cols, 16, false};
+    b[k++] = {token_rows, 8 * n_tokens * top_k, 8, false};
+    b[k++] = {weights, 4 * n_tokens * top_k, 4, false};
+    b[k++] = {d_rows, esz * total_rows * cols, 16, true};
+    b[k++] = {d_weights, 4 * n_tokens * top_k, 4, true};
+    if (seg_offsets)
+        b[k++] = {seg_offsets, 8 * (n_groups + 1), 8, false};
+    st = check_bufs(b, k);
+    if (st != MXQ_OK)
+        return st;
+    return launched(mxq::launch_moe_combine_backward(
+        dtype == MXQ_OUT_BF16, d_out, rows, total_rows, token_rows, weights, seg_offsets,
+        n_groups, n_tokens, top_k, cols, d_rows, d_weights, (hipStream_t)stream));
+}
+
+// The activation operand of the few-row products: format, pointers, then
+// (after the sizes) its buffers appended to b.
+static int act_args(int x_fmt, const void *x, const uint8_t *xbs, const float *xs)
+{
+    if (x_fmt != MXQ_X_BF16 && x_fmt != MXQ_X_F32 && x_fmt != MXQ_X_NVFP4)
+        return MXQ_ERR_ARG;
+    if (!x || (x_fmt == MXQ_X_NVFP4 && (!xbs || !xs)))
+        return MXQ_ERR_NULL;
+    if (x_fmt != MXQ_X_NVFP4 && (xbs || xs))
+        return MXQ_ERR_OFFSETS;
+    return MXQ_OK;
+}
+static int act_bufs(Buf *b, const mxq::ActX &x, int64_t rows, int64_t K)
+{
+    if (x.fmt == MXQ_X_NVFP4) {
+        b[0] = {x.x, rows * (K / 2), 16, false};
+        b[1] = {x.bs, rows * (K / 16), 4, false};
+        b[2] = {x.s, 4 * rows, 4, false};
+        return 3;
+    }
+    b[0] = {x.x, rows * K * (x.fmt == MXQ_X_F32 ? 4 : 2), 16, false};
+    return 1;
+}
+
+int mxq_nvfp4_matvec(int x_fmt, const void *x, const uint8_t *x_block_scales,
+                     const float *x_scales, const uint8_t *b, const uint8_t *b_block_scales,
+                     const float *b_scales, int64_t rows_per_b_scale, int64_t M, int64_t N,
+                     int64_t K, int out_dtype, void *c, void *stream)
+{
+    if (!dtype_ok(out_dtype))
+        return MXQ_ERR_ARG;
+    int st = act_args(x_fmt, x, x_block_scales, x_scales);
+    if (st != MXQ_OK)
+        return st;
+    if (!b || !b_block_scales || !b_scales || !c)
+        return MXQ_ERR_NULL;
+    if (M < 1 || M > MAX_MATVEC_ROWS || N < 1 || N > MAX_MATVEC_N || K < 1 || K > MAX_MATVEC_K ||
+        rows_per_b_scale < 1)
+        return MXQ_ERR_SIZE;
+    if (K % 64 != 0)
+        return MXQ_ERR_SHAPE;
+    const mxq::ActX ax{x_fmt, x, x_block_scales, x_scales};
+    const int esz = out_dtype == MXQ_OUT_F32 ? 4 : 2;
+    Buf bb[7];
+    int k = act_bufs(bb, ax, M, K);
+    bb[k++] = {b, N * (K / 2), 16, false};
+    bb[k++] = {b_block_scales, N * (K / 16), 4, false};
+    bb[k++] = {b_scales, 4 * ((N - 1) / rows_per_b_scale + 1), 4, false};
+    bb[k++] = {c, esz * M * N, esz, true};
+    st = check_bufs(bb, k);
+    if (st != MXQ_OK)
+        return st;
+    return launched(mxq::launch_nvfp4_matvec(ax, mxq::WeightB{b, b_block_scales}, b_scales,
+                                             rows_per_b_scale, M, N, K,
+                                             out_dtype == MXQ_OUT_BF16, c, (hipStream_t)stream));
+}
+
+static bool expert_sizes_ok(int64_t n_groups, int64_t total_rows, int64_t N, int64_t K)
+{
+    return n_groups >= 1 && n_groups <= MAX_MATVEC_GROUPS && total_rows >= 1 &&
+           total_rows <= mxq::MAX_COPIES && N >= 1 && N <= MAX_MATVEC_N && K >= 1 &&
+           K <= MAX_MATVEC_K && mxq::expert_grid_ok(n_groups, total_rows, N);
+}
+
+int mxq_nvfp4_expert_matvec(int x_fmt, const void *x, const uint8_t *x_block_scales,
+                            const float *x_scales, const uint8_t *b,
+                            const uint8_t *b_block_scales, const float *b_scales,
+                            const int64_t *seg_offsets, int64_t n_groups, int64_t total_rows,
+                            int64_t N, int64_t K, int out_dtype, void *c, void *stream)
+{
+    if (!dtype_ok(out_dtype))
+        return MXQ_ERR_ARG;
+    int st = act_args(x_fmt, x, x_block_scales, x_scales);
+    if (st != MXQ_OK)
+        return st;
+    if (!b || !b_block_scales || !b_scales || !seg_offsets || !c)
+        return MXQ_ERR_NULL;
+    if (!expert_sizes_ok(n_groups, total_rows, N, K))
+        return MXQ_ERR_SIZE;
+    if (K % 64 != 0)
+        return MXQ_ERR_SHAPE;
+    const mxq::ActX ax{x_fmt, x, x_block_scales, x_scales};
+    const int esz = out_dtype == MXQ_OUT_F32 ? 4 : 2;
+    Buf bb[8];
+    int k = act_bufs(bb, ax, total_rows, K);
+    bb[k++] = {b, n_groups * N * (K / 2), 16, false};
+    bb[k++] = {b_block_scales, n_groups * N * (K / 16), 4, false};
+    bb[k++] = {b_scales, 4 * n_groups, 4, false};
+    bb[k++] = {seg_offsets, 8 * (n_groups + 1), 8, false};
+    bb[k++] = {c, esz * total_rows * N, esz, true};
+    st = check_bufs(bb, k);
+    if (st != MXQ_OK)
+        return st;
+    return launched(mxq::launch_nvfp4_expert_matvec(
+        ax, total_rows, nullptr, seg_offsets, n_groups, total_rows,
+        mxq::WeightB{b, b_block_scales}, mxq::WeightB{nullptr, nullptr}, b_scales, N, K,
+        out_dtype == MXQ_OUT_BF16, c, (hipStream_t)stream));
+}
+
+int mxq_nvfp4_expert_gateup(int x_fmt, const void *x, const uint8_t *x_block_scales,
+                            const float *x_scales, int64_t n_tokens, const int64_t *row_tokens,
+                            const int64_t *seg_offsets, int64_t n_groups, int64_t total_rows,
+                            const uint8_t *gate, const uint8_t *gate_block_scales,
+                            const uint8_t *up, const uint8_t *up_block_scales,
+                            const float *scope_scales, int64_t N, int64_t K, int out_dtype,
+                            void *h, void *stream)
+{
+    if (!dtype_ok(out_dtype))
+        return MXQ_ERR_ARG;
+    int st = act_args(x_fmt, x, x_block_scales, x_scales);
+    if (st != MXQ_OK)
+        return st;
+    if (!row_tokens || !seg_offsets || !gate || !gate_block_scales || !up || !up_block_scales ||
+        !scope_scales || !h)
+        return MXQ_ERR_NULL;
+    if (n_tokens < 1 || n_tokens > mxq::MAX_COPIES ||
+        !expert_sizes_ok(n_groups, total_rows, N, K))
+        return MXQ_ERR_SIZE;
+    if (K % 64 != 0)
+        return MXQ_ERR_SHAPE;
+    const mxq::ActX ax{x_fmt, x, x_block_scales, x_scales};
+    const int esz = out_dtype == MXQ_OUT_F32 ? 4 : 2;
+    Buf bb[11];
+    int k = act_bufs(bb, ax, n_tokens, K);
+    bb[k++] = {row_tokens, 8 * total_rows, 8, false};
+    bb[k++] = {seg_offsets, 8 * (n_groups + 1), 8, false};
+    bb[k++] = {gate, n_groups * N * (K / 2), 16, false};
+    bb[k++] = {gate_block_scales, n_groups * N * (K / 16), 4, false};
+    bb[k++] = {up, n_groups * N * (K / 2), 16, false};
+    bb[k++] = {up_block_scales, n_groups * N * (K / 16), 4, false};
+    bb[k++] = {scope_scales, 4 * n_groups, 4, false};
+    bb[k++] = {h, esz * total_rows * N, esz, true};
+    st = check_bufs(bb, k);
+    if (st != MXQ_OK)
+        return st;
+    return launched(mxq::launch_nvfp4_expert_matvec(
+        ax, n_tokens, row_tokens, seg_offsets, n_groups, total_rows,
+        mxq::WeightB{gate, gate_block_scales}, mxq::WeightB{up, up_block_scales}, scope_scales,
+        N, K, out_dtype == MXQ_OUT_BF16, h, (hipStream_t)stream));
+}
+
+// Status of the attention's sizes (without the pages, which only the call has).
+static int attention_sizes(int64_t n_seqs, int64_t q_len, int64_t n_heads, int64_t n_kv_heads,
+                           int64_t head_dim, int64_t max_keys)
+{
+    if (n_seqs < 1 || q_len < 1 || n_heads < 1 || n_kv_heads < 1 || max_keys < 1 ||
+        n_seqs > MAX_ATTN_ROWS || q_len > MAX_ATTN_ROWS || n_heads > MAX_ATTN_ROWS ||
+        n_seqs * q_len > MAX_ATTN_ROWS || n_seqs * q_len * n_heads > MAX_ATTN_ROWS ||
+        max_keys > MAX_ATTN_KEYS)
+        return MXQ_ERR_SIZE;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || n_heads % n_kv_heads != 0)
+        return MXQ_ERR_SHAPE;
+    return MXQ_OK;
+}
+
+int64_t mxq_nvfp4_attention_workspace(int64_t n_seqs, int64_t q_len, int64_t n_heads,
+                                      int64_t n_kv_heads, int64_t head_dim, int64_t max_keys)
+{
+    if (attention_sizes(n_seqs, q_len, n_heads, n_kv_heads, head_dim, max_keys) != MXQ_OK)
+        return 0;
+    return mxq::nvfp4_attention_workspace(n_seqs, q_len, n_heads, n_kv_heads, head_dim, max_keys);
+}
+
+int mxq_nvfp4_attention(const uint16_t *q, const mxq_nvfp4_cache *k, const mxq_nvfp4_cache *v,
+                        const int64_t *block_table, const int64_t *seq_lens, int64_t n_seqs,
+                        int64_t q_len, int64_t n_heads, int64_t n_kv_heads, int64_t head_dim,
+                        int64_t n_pages, int64_t page_size, int64_t max_pages,
+                        float softmax_scale, int causal, int64_t window, uint16_t *out,
+                        float *lse, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!q || !k || !v || !block_table || !seq_lens || !out || !k->codes || !k->block_scales ||
+        !k->scales || !v->codes || !v->block_scales || !v->scales)
+        return MXQ_ERR_NULL;
+    if (!finite_f32(softmax_scale))
+        return MXQ_ERR_ARG;
+    if (softmax_scale <= 0.0f || window < 0 || (!causal && window != 0))
+        return MXQ_ERR_ARG;
+    if (n_pages < 1 || page_size < 1 || max_pages < 1 || n_kv_heads < 1 ||
+        page_size > MAX_ATTN_KEYS || max_pages > MAX_ATTN_KEYS / page_size ||
+        n_kv_heads > MAX_ATTN_ROWS || n_pages > MAX_CACHE_ROWS / page_size / n_kv_heads)
+        return MXQ_ERR_SIZE;
+    const int sz = attention_sizes(n_seqs, q_len, n_heads, n_kv_heads, head_dim,
+                                   max_pages * page_size);
+    if (sz != MXQ_OK)
+        return sz;
+    if (page_size % 16 != 0)
+        return MXQ_ERR_SHAPE;
+    const int64_t need = mxq::nvfp4_attention_workspace(n_seqs, q_len, n_heads, n_kv_heads,
+                                                        head_dim, max_pages * page_size);
+    if (need > 0 && !workspace)
+        return MXQ_ERR_NULL;
+    if (workspace_bytes < need)
+        return MXQ_ERR_SIZE;
+    const int64_t rows = n_pages * n_kv_heads * page_size, nq = n_seqs * q_len * n_heads;
+    Buf b[13];
+    int i = 0;
+    b[i++] = {q, 2 * nq * head_dim, 16, false};
+    for (const mxq_nvfp4_cache *c : {k, v}) {
+        b[i++] = {c->codes, rows * (head_dim / 2), 16, false};
+        b[i++] = {c->block_scales, rows * (head_dim / 16), 8, false};
+        b[i++] = {c->scales, 4 * rows, 16, false};
+    }
+    b[i++] = {block_table, 8 * n_seqs * max_pages, 8, false};
+    b[i++] = {seq_lens, 8 * n_seqs, 8, false};
+    b[i++] = {out, 2 * nq * head_dim, 16, true};
+    if (lse)
+        b[i++] = {lse, 4 * nq, 4, true};
+    if (need > 0)
+        b[i++] = {workspace, need, 16, true};
+    const int st = check_bufs(b, i);
+    if (st != MXQ_OK)
+        return st;
+    const mxq::AttnArgs a{q, k->codes, k->block_scales, k->scales, v->codes, v->block_scales,
+                          v->scales, block_table, seq_lens, n_seqs, q_len, n_heads, n_kv_heads,
+                          head_dim, n_pages, page_size, max_pages, softmax_scale, causal != 0,
+                          window, out, lse};
+    return launched(mxq::launch_nvfp4_attention(a, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"
