@@ -778,7 +778,8 @@ typedef struct {
  *   the length may hold anything.
  *   softmax_scale > 0; window >= 0, and 0 if not causal (MXQ_ERR_ARG).
  *   workspace: mxq_nvfp4_attention_workspace(...) bytes.
- *   n_seqs * q_len * n_heads <= 2^25, cache rows <= 2^40.
+ *   n_seqs * q_len * n_heads <= 2^25, max_pages * page_size <= 2^30, cache rows
+ *   <= 2^40.
  * Scores, the running maximum and sum and the output are fp32; q is held in FP16 under
  * a power-of-two scale per row (as BF16 activations above) and the softmax's
  * numerators in FP16 (2^-11 relative) under the running maximum of their

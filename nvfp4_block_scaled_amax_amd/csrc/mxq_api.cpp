@@ -34,7 +34,7 @@ constexpr int64_t MAX_COPY_FLOOR_BYTES = (int64_t)1 << 35;
 constexpr int64_t MAX_LAYER_TOKENS = (int64_t)1 << 24;
 constexpr int64_t MAX_MATVEC_ROWS = 64, MAX_MATVEC_N = (int64_t)1 << 24;
 constexpr int64_t MAX_MATVEC_K = (int64_t)1 << 16, MAX_MATVEC_GROUPS = (int64_t)1 << 16;
-constexpr int64_t MAX_ATTN_ROWS = (int64_t)1 << 25, MAX_ATTN_KEYS = (int64_t)1 << 31;
+constexpr int64_t MAX_ATTN_ROWS = (int64_t)1 << 25, MAX_ATTN_KEYS = (int64_t)1 << 30;
 constexpr int64_t MAX_CACHE_ROWS = (int64_t)1 << 40;
 
 bool size_ok(int64_t a, int64_t b)

@@ -1,7 +1,40 @@
 // mxq_attention.hip -- attention over a paged cache of NVFP4 keys and values
 // (rows as the per-token quantizer writes them: codes, E4M3 block scales, one
-// FP32 scale).  One wavefront per (sequence, query, head) walks the keys with
-// the running maximum and sum of an online softmax.
+// FP32 scale).
+//
+// Mathematics.  A wavefront keeps 16 RT query rows (the queries of one
+// key/value head: q_len times the heads that share it) and walks keys 32 at a
+// time.  S^T = K q^T and O^T += V^T P^T are 16x16x32 FP16 matrix instructions
+// with the cache as their first operand, so that a query row is a lane
+// column (lane % 16) throughout: the softmax's row maximum and sum are over a
+// lane's own registers and the four lanes l, l + 16, l + 32, l + 48, and P
+// leaves the first product's accumulators in the layout the second takes
+// (its contraction index, the key, may come in any order that both operands
+// share: slot j of lane group g is key 4g + j of the tile's first 16 keys
+// for j < 4, of its second 16 otherwise).
+//   dec(code) dec(block scale) is an exact FP16 value (6 significant bits).
+// The FP32 scales stay out of the products: a key's scale multiplies its
+// scores, a value's scale multiplies the softmax's numerators p, which are
+// rounded to FP16 as p s_v 2^(14-E), with E the exponent of the running
+// maximum of p s_v, tracked beside the running maximum of the scores: the
+// largest numerator lands in [2^14, 2^15), and one within 2^-28 of it keeps
+// all its 11 bits whatever the scales are.  A step with smaller ones (whose
+// values may be all that an output element is made of, where the others'
+// codes are 0) takes those in a second round of products under 2^29.  q is exact in FP16 under a
+// power of two per row.
+//   Operand order.  A lane reads the D/4 consecutive elements of a key that
+// belong to its group (one 16-byte load at D = 128) and the queries are
+// loaded in the same order.  Of a value row lane l reads elements D/16 l
+// onwards; two keys' nibbles are merged byte-wise (even and odd elements),
+// so that one conversion yields the pair (key t, key t + 1) of one element,
+// which is what the second product's first operand holds.  Nothing of the
+// cache passes through LDS.
+//
+// Split.  A workgroup of four wavefronts takes a chunk of the keys of one
+// (sequence, key/value head, row tile), its wavefronts every fourth tile;
+// they join through LDS.  With one chunk the workgroup writes the result,
+// otherwise partial results go to the workspace and a second kernel joins
+// them.
 #include "mxq_layer.h"
 #include "mxq_layer_device.h"
 
@@ -9,74 +42,585 @@ namespace mxq {
 
 namespace {
 
-template <int D>
-__global__ void __launch_bounds__(64) nvfp4_attention_kernel(AttnArgs a)
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int ATT_WAVES = 4, ATT_THREADS = 64 * ATT_WAVES;
+constexpr int ATT_TILE = 32;                        // keys per step of a wavefront
+constexpr int ATT_MIN_CHUNK = 2 * ATT_TILE * ATT_WAVES;
+constexpr int64_t ATT_TARGET_WGS = 2048;
+constexpr float NO_MAX = -1.0e30f;                  // running maximum before the first key
+constexpr float LOW = 0x1p-14f, LOW_UP = 0x1p29f;   // numerators of the second round
+
+struct AttnK {
+    const uint16_t *q;
+    const uint8_t *k, *kbs;
+    const float *ks;
+    const uint8_t *v, *vbs;
+    const float *vs;
+    const int64_t *table, *lens;
+    int64_t n_pages, max_pages;
+    int q_len, n_heads, n_kv_heads, group, page_size, rows;   // rows = q_len * group
+    Div page_div, group_div;
+    float scale;                                     // softmax_scale * log2 e
+    int causal, window;
+    int chunk, n_chunks, row_tiles;
+    uint16_t *out;
+    float *lse;
+    float *part_ml, *part_o;                         // [row][chunk][2], [row][chunk][D]
+};
+
+__device__ __forceinline__ float max4_groups(float v)
 {
-    constexpr int V = D / 64;                       // values per lane
-    const uint32_t lane = lane_id();
-    const int64_t id = wg_id();
-    const int64_t head = id % a.n_heads, qi = id / a.n_heads % a.q_len,
-                  b = id / a.n_heads / a.q_len;
-    const int64_t kvh = head / (a.n_heads / a.n_kv_heads);
-    int64_t len = a.seq_lens[b];
-    const int64_t cap = a.max_pages * a.page_size;
-    len = len < 0 ? 0 : len > cap ? cap : len;
-    const int64_t pos = len - a.q_len + qi;
-    const int64_t hi = a.causal ? pos + 1 : len;
-    int64_t lo = a.window > 0 ? pos - a.window + 1 : 0;
-    lo = lo < 0 ? 0 : lo;
-    float q[V], o[V] = {};
+    uint2_t r = __builtin_amdgcn_permlane16_swap(f2u(v), f2u(v), false, false);
+    v = __builtin_fmaxf(u2f(r[0]), u2f(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
+    return __builtin_fmaxf(u2f(r[0]), u2f(r[1]));
+}
+__device__ __forceinline__ float sum4_groups(float v) { return sum32_f32(sum16_f32(v)); }
+
+// One tile's cache data of a lane.
+template <int D>
+struct KvTile {
+    static constexpr int KW = D / 32;                // dwords of a key's codes per lane
+    static constexpr int VB = D / 32;                // bytes of a value's codes per lane
+    uint32_t kc[2][KW], kb[2];
+    f32x4_t ks[2], vs[2];
+    uint32_t vc[8][VB > 4 ? VB / 4 : 1], vb[8];
+};
+
+// Rows of the tile's two 16-key halves: wave-uniform base rows in the cache.
+struct TileRows {
+    int64_t r[2];
+};
+__device__ __forceinline__ TileRows tile_rows(const AttnK &a, const int64_t *table, int kvh,
+                                              int t0)
+{
+    TileRows o;
+    const int last = (int)(a.max_pages * a.page_size) - 16;
 #pragma unroll
-    for (int j = 0; j < V; j++)
-        q[j] = u2f((uint32_t)a.q[id * D + lane * V + j] << 16);
-    float m = -3.0e38f, l = 0.0f;
-    for (int64_t t = lo; t < hi; t++) {
-        int64_t page = a.block_table[b * a.max_pages + t / a.page_size];
+    for (int s = 0; s < 2; s++) {
+        int t = t0 + 16 * s;
+        t = t < last ? t : last;                     // halves past the table: masked by length
+        const uint32_t pi = udiv((uint32_t)t, a.page_div);
+        int64_t page = table[pi];
         page = page < 0 ? 0 : page >= a.n_pages ? a.n_pages - 1 : page;
-        const int64_t row = (page * a.n_kv_heads + kvh) * a.page_size + t % a.page_size;
-        auto value = [&](const uint8_t *codes, const uint8_t *bs, int j) {
-            const int d = (int)lane * V + j;
-            const uint32_t c = codes[row * (D / 2) + d / 2];
-            return e2m1_values(c)[d & 1] * e4m3_value(bs[row * (D / 16) + d / 16]);
-        };
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; j++)
-            s = __builtin_fmaf(q[j], value(a.k, a.kbs, j), s);
-        s = wave_sum_f32(s) * a.ks[row] * a.scale;
-        const float mn = s > m ? s : m;
-        const float al = exp_f32(m - mn), p = exp_f32(s - mn);
-        m = mn;
-        l = l * al + p;
-        const float pv = p * a.vs[row];
-#pragma unroll
-        for (int j = 0; j < V; j++)
-            o[j] = o[j] * al + pv * value(a.v, a.vbs, j);
+        o.r[s] = (page * a.n_kv_heads + kvh) * a.page_size + (t - (int)pi * a.page_size);
     }
-    const float r = l > 0.0f ? 1.0f / l : 0.0f;
+    return o;
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(KvTile<D> &x, const AttnK &a, const TileRows &rows,
+                                          int l, int g)
+{
+    constexpr int KW = KvTile<D>::KW, VB = KvTile<D>::VB;
+#pragma unroll
+    for (int s = 0; s < 2; s++) {
+        const int64_t r = rows.r[s];
+        const uint8_t *kc = a.k + r * (D / 2) + (uint32_t)(l * (D / 2) + g * (D / 8));
+        const uint8_t *kb = a.kbs + r * (D / 16) + (uint32_t)(l * (D / 16) + g * (D / 64));
+        if constexpr (KW == 2) {
+            const uint2 c = ld8(kc);
+            x.kc[s][0] = c.x;
+            x.kc[s][1] = c.y;
+            x.kb[s] = *kb;
+        } else {
+#pragma unroll
+            for (int j = 0; j < KW / 4; j++) {
+                const uint4 c = ld16(kc + 16 * j);
+                x.kc[s][4 * j] = c.x;
+                x.kc[s][4 * j + 1] = c.y;
+                x.kc[s][4 * j + 2] = c.z;
+                x.kc[s][4 * j + 3] = c.w;
+            }
+            if constexpr (KW == 4)
+                x.kb[s] = *reinterpret_cast<const uint16_t *>(kb);
+            else
+                x.kb[s] = *reinterpret_cast<const uint32_t *>(kb);
+        }
+        x.ks[s] = *reinterpret_cast<const f32x4_t *>(a.ks + r + 4 * g);
+        x.vs[s] = *reinterpret_cast<const f32x4_t *>(a.vs + r + 4 * g);
+        const uint8_t *vc = a.v + r * (D / 2) + (uint32_t)(4 * g * (D / 2) + l * VB);
+        const uint8_t *vb = a.vbs + r * (D / 16) + (uint32_t)(4 * g * (D / 16) + l * (D / 16) / 16);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint8_t *p = vc + i * (D / 2);
+            if constexpr (VB == 2)
+                x.vc[4 * s + i][0] = *reinterpret_cast<const uint16_t *>(p);
+            else if constexpr (VB == 4)
+                x.vc[4 * s + i][0] = *reinterpret_cast<const uint32_t *>(p);
+            else {
+                const uint2 c = ld8(p);
+                x.vc[4 * s + i][0] = c.x;
+                x.vc[4 * s + i][1] = c.y;
+            }
+            x.vb[4 * s + i] = vb[i * (D / 16)];
+        }
+    }
+}
+
+// E4M3 byte -> FP16 (exact).
+__device__ __forceinline__ _Float16 e4m3_f16(uint32_t byte) { return (_Float16)e4m3_value(byte); }
+
+template <int J>
+__device__ __forceinline__ f16x2_t pair_f16(uint32_t codes)
+{
+    return __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, J));
+}
+__device__ __forceinline__ f16x8_t cat8(f16x2_t a, f16x2_t b, f16x2_t c, f16x2_t d)
+{
+    return f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// Eight elements (one dword of codes) under one block scale.
+__device__ __forceinline__ f16x8_t oct_f16(uint32_t codes, f16x2_t d)
+{
+    return cat8(pair_f16<0>(codes) * d, pair_f16<1>(codes) * d, pair_f16<2>(codes) * d,
+                pair_f16<3>(codes) * d);
+}
+__device__ __forceinline__ f16x2_t pair_f16_dyn(uint32_t codes, int j)
+{
+    return j == 0 ? pair_f16<0>(codes) : j == 1 ? pair_f16<1>(codes)
+         : j == 2 ? pair_f16<2>(codes) : pair_f16<3>(codes);
+}
+
+// State of a wavefront's 16 RT rows.  Row (lane % 16) of tile rt: running
+// maximum m of the scores (log2 units), this lane's part of the sum l, the
+// running maximum w of p s_v relative to m, and O^T in units of 2^(e - 14).
+template <int D, int RT>
+struct Rows {
+    f16x8_t q[RT][D / 32];
+    float c[RT];                                     // score factor of the row
+    float m[RT], l[RT], w[RT];
+    int e[RT];
+    f32x4_t o[RT][D / 16];
+};
+
+template <int D, int RT, bool MASKED>
+__device__ __forceinline__ void attend(Rows<D, RT> &st, const KvTile<D> &x, int t0, int len,
+                                       const int (&lo)[RT], const int (&hi)[RT], int g)
+{
+    constexpr int KK = D / 32;
+    // Scores: two 16-key halves, KK steps of 8 elements per lane group.
+    f32x4_t s[2][RT];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++)
+            s[h][rt] = f32x4_t{};
+#pragma unroll
+        for (int kk = 0; kk < KK; kk++) {
+            // The D/4 elements of a lane hold D/64 blocks of 16 (two dwords each).
+            const _Float16 d = e4m3_f16((x.kb[h] >> (8 * (kk / 2))) & 0xFFu);
+            const f16x8_t kf = oct_f16(x.kc[h][kk], f16x2_t{d, d});
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+                s[h][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, st.q[rt][kk], s[h][rt], 0, 0,
+                                                                   0);
+        }
+    }
+    f32x4_t vs[2] = {x.vs[0], x.vs[1]};
+    if constexpr (MASKED) {
+        // Slots past the length may hold anything: their value scales count as 0.
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (t0 + 16 * (j >> 2) + 4 * g + (j & 3) >= len)
+                vs[j >> 2][j & 3] = 0.0f;
+    }
+    f16x8_t p8[RT], p8lo[RT];
+    bool any_low = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        float z[8], tm = NO_MAX;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            z[j] = s[j >> 2][rt][j & 3] * (x.ks[j >> 2][j & 3] * st.c[rt]);
+            if constexpr (MASKED) {
+                const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
+                z[j] = t >= lo[rt] && t < hi[rt] ? z[j] : NO_MAX;
+            }
+            tm = __builtin_fmaxf(tm, z[j]);
+        }
+        tm = max4_groups(tm);
+        const float mn = __builtin_fmaxf(st.m[rt], tm);
+        const float al = __builtin_amdgcn_exp2f(st.m[rt] - mn);
+        float sum = 0.0f, pw[8], wm = 0.0f, pm = 1.0e30f;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            float p = __builtin_amdgcn_exp2f(z[j] - mn);
+            if constexpr (MASKED)
+                p = z[j] == NO_MAX ? 0.0f : p;
+            sum += p;
+            pw[j] = p * vs[j >> 2][j & 3];
+            wm = __builtin_fmaxf(wm, pw[j]);
+            pm = __builtin_fminf(pm, pw[j]);
+        }
+        wm = max4_groups(wm);
+        const float wn = __builtin_fmaxf(st.w[rt] * al, wm);
+        int e = (int)(f2u(wn) >> 23) - 127;
+        // Twelve binades above the smallest normal number: 2^(14 - e) stays finite.
+        e = e < -112 ? -112 : e;
+        const float up = u2f((uint32_t)(14 - e + 127) << 23);       // 2^(14 - e)
+        const float f = __builtin_ldexpf(al, st.e[rt] - e);
+        st.m[rt] = mn;
+        st.l[rt] = __builtin_fmaf(st.l[rt], al, sum);
+        st.w[rt] = wn;
+        st.e[rt] = e;
+#pragma unroll
+        for (int j = 0; j < D / 16; j++)
+            st.o[rt][j] *= f;
+        p8lo[rt] = f16x8_t{};
+        if (__builtin_amdgcn_ballot_w64(pm * up < LOW) != 0) {      // zeros too: harmless
+            any_low = true;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float x = pw[j] * up;
+                p8lo[rt][j] = (_Float16)(x < LOW ? x * LOW_UP : 0.0f);
+                p8[rt][j] = (_Float16)(x < LOW ? 0.0f : x);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                p8[rt][j] = (_Float16)(pw[j] * up);
+        }
+    }
+    // Values: pairs of keys (2i, 2i + 1) of the lane group's eight.
+    f16x2_t vd[4];
+    uint32_t ev[4][KvTile<D>::VB > 4 ? 2 : 1], od[4][KvTile<D>::VB > 4 ? 2 : 1];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint32_t b0 = x.vb[2 * i], b1 = x.vb[2 * i + 1];
+        if constexpr (MASKED) {
+            const int t = t0 + 16 * (i >> 1) + 4 * g + 2 * (i & 1);
+            b0 = t < len ? b0 : 0;
+            b1 = t + 1 < len ? b1 : 0;
+        }
+        vd[i] = f16x2_t{e4m3_f16(b0), e4m3_f16(b1)};
+#pragma unroll
+        for (int wd = 0; wd < (KvTile<D>::VB > 4 ? 2 : 1); wd++) {
+            const uint32_t c0 = x.vc[2 * i][wd], c1 = x.vc[2 * i + 1][wd];
+            ev[i][wd] = (c0 & 0x0F0F0F0Fu) | ((c1 << 4) & 0xF0F0F0F0u);
+            od[i][wd] = ((c0 >> 4) & 0x0F0F0F0Fu) | (c1 & 0xF0F0F0F0u);
+        }
+    }
+    auto values = [&](int j) {
+        f16x2_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            v[i] = pair_f16_dyn((j & 1) ? od[i][j >> 3] : ev[i][j >> 3], (j >> 1) & 3) * vd[i];
+        return cat8(v[0], v[1], v[2], v[3]);
+    };
+#pragma unroll
+    for (int j = 0; j < D / 16; j++) {
+        const f16x8_t vf = values(j);
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++)
+            st.o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p8[rt], st.o[rt][j], 0, 0, 0);
+    }
+    if (any_low) {
+#pragma unroll
+        for (int j = 0; j < D / 16; j++) {
+            const f16x8_t vf = values(j);
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++) {
+                const f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p8lo[rt], f32x4_t{},
+                                                                         0, 0, 0);
+                st.o[rt][j] += o * (1.0f / LOW_UP);
+            }
+        }
+    }
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
+    nvfp4_attention_kernel(AttnK a)
+{
+    constexpr int ROWS = 16 * RT;
+    __shared__ float lds_ml[ATT_WAVES][ROWS][2];
+    // Rows padded by four floats: the 16 rows a store touches miss each other's banks.
+    __shared__ __attribute__((aligned(16))) float lds_o[ATT_WAVES][ROWS][D + 4];
+
+    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
+    uint32_t id = wg_id();
+    const int tile = (int)(id % (uint32_t)a.row_tiles);
+    id /= (uint32_t)a.row_tiles;
+    const int chunk = (int)(id % (uint32_t)a.n_chunks);
+    id /= (uint32_t)a.n_chunks;
+    const int kvh = (int)(id % (uint32_t)a.n_kv_heads), b = (int)(id / (uint32_t)a.n_kv_heads);
+
+    const int64_t cap = a.max_pages * a.page_size;
+    int64_t len64 = a.lens[b];
+    len64 = len64 < 0 ? 0 : len64 > cap ? cap : len64;
+    const int len = (int)len64;
+
+    // Keys the tile's rows see: [kmin, kmax); this workgroup's part of them.
+    const int r0 = tile * ROWS;
+    const int r1 = r0 + ROWS < a.rows ? r0 + ROWS : a.rows;
+    const int first = len - a.q_len + (int)udiv((uint32_t)r0, a.group_div);
+    const int last = len - a.q_len + (int)udiv((uint32_t)(r1 - 1), a.group_div);
+    const int kmax = a.causal ? (last + 1 < 0 ? 0 : last + 1) : len;
+    int kmin = a.causal && a.window > 0 ? first - a.window + 1 : 0;
+    kmin = kmin < 0 ? 0 : kmin & ~(ATT_TILE - 1);
+    const int64_t start64 = (int64_t)kmin + (int64_t)chunk * a.chunk;
+    const int start = start64 < kmax ? (int)start64 : kmax;
+    const int stop = kmax - start < a.chunk ? kmax : start + a.chunk;
+
+    Rows<D, RT> st;
+    int lo[RT], hi[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int r = r0 + 16 * rt + l < a.rows ? r0 + 16 * rt + l : a.rows - 1;
+        const int qi = (int)udiv((uint32_t)r, a.group_div);
+        const int pos = len - a.q_len + qi;
+        hi[rt] = a.causal ? pos + 1 : len;
+        lo[rt] = a.causal && a.window > 0 ? pos - a.window + 1 : 0;
+        const int64_t qrow = ((int64_t)b * a.q_len + qi) * a.n_heads + kvh * a.group +
+                             (r - qi * a.group);
+        const uint16_t *qp = a.q + qrow * D + g * (D / 4);
+        uint4 raw[D / 32];
+        uint32_t am = 0;
+#pragma unroll
+        for (int kk = 0; kk < D / 32; kk++) {
+            raw[kk] = ld16(qp + 8 * kk);
+            am = pk_max_u16(am, pk_max_u16(pk_max_u16(raw[kk].x & 0x7FFF7FFFu,
+                                                      raw[kk].y & 0x7FFF7FFFu),
+                                           pk_max_u16(raw[kk].z & 0x7FFF7FFFu,
+                                                      raw[kk].w & 0x7FFF7FFFu)));
+        }
+        am = max32_u32(max16_u32(hmax_u16(am)));
+        // Largest magnitude into [2^14, 2^15): exact for values within 2^-31 of it.
+        const int e = (int)(am >> 7) - 127 - 14;
+        st.c[rt] = __builtin_ldexpf(a.scale, e);
+#pragma unroll
+        for (int kk = 0; kk < D / 32; kk++) {
+            const uint32_t w[4] = {raw[kk].x, raw[kk].y, raw[kk].z, raw[kk].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                st.q[rt][kk][2 * i] = (_Float16)__builtin_ldexpf(bf16_lo(w[i]), -e);
+                st.q[rt][kk][2 * i + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[i]), -e);
+            }
+        }
+        st.m[rt] = NO_MAX;
+        st.l[rt] = 0.0f;
+        st.w[rt] = 0.0f;
+        st.e[rt] = -112;
+#pragma unroll
+        for (int j = 0; j < D / 16; j++)
+            st.o[rt][j] = f32x4_t{};
+    }
+
+    const int64_t *table = a.table + (int64_t)b * a.max_pages;
+    constexpr int STEP = ATT_TILE * ATT_WAVES;
+    // Keys every row sees: a tile inside [full_lo, full_hi) needs no mask.
+    const int full_hi = a.causal ? (first + 1 < len ? first + 1 : len) : len;
+    const int full_lo = a.causal && a.window > 0 ? last - a.window + 1 : 0;
+    int t0 = start + wave * ATT_TILE;
+    if (t0 < stop) {
+        KvTile<D> x;
+        load_tile<D>(x, a, tile_rows(a, table, kvh, t0), l, g);
+        for (; t0 < stop; t0 += STEP) {
+            // The next tile's loads are in flight while this one is worked on (the
+            // last step reads its own tile again).
+            const int tn = t0 + STEP < stop ? t0 + STEP : t0;
+            KvTile<D> nx;
+            load_tile<D>(nx, a, tile_rows(a, table, kvh, tn), l, g);
+            if (t0 >= full_lo && t0 + ATT_TILE <= full_hi)
+                attend<D, RT, false>(st, x, t0, len, lo, hi, g);
+            else
+                attend<D, RT, true>(st, x, t0, len, lo, hi, g);
+            x = nx;
+        }
+    }
+
+    // Join the four wavefronts.
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        st.l[rt] = sum4_groups(st.l[rt]);
+        if (g == 0) {
+            lds_ml[wave][16 * rt + l][0] = st.m[rt];
+            lds_ml[wave][16 * rt + l][1] = st.l[rt];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int r = 16 * rt + l;
+        float m = NO_MAX;
+#pragma unroll
+        for (int w = 0; w < ATT_WAVES; w++)
+            m = __builtin_fmaxf(m, lds_ml[w][r][0]);
+        const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(st.m[rt] - m), st.e[rt] - 14);
+        // Element 4g + i of lane column l, tile j: d = (4g + i) D/16 + j.
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                lds_o[wave][r][(4 * g + i) * (D / 16) + j] = st.o[rt][j][i] * f;
+    }
+    __syncthreads();
+    constexpr int PER = D / 8;                       // 8 elements per thread
+    for (int i = (int)tid(); i < (r1 - r0) * PER; i += ATT_THREADS) {
+        const int r = i / PER, d = 8 * (i % PER);
+        float m = NO_MAX, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < ATT_WAVES; w++)
+            m = __builtin_fmaxf(m, lds_ml[w][r][0]);
+#pragma unroll
+        for (int w = 0; w < ATT_WAVES; w++)
+            sum += lds_ml[w][r][1] * __builtin_amdgcn_exp2f(lds_ml[w][r][0] - m);
+        float o[8] = {};
+#pragma unroll
+        for (int w = 0; w < ATT_WAVES; w++)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                o[j] += lds_o[w][r][d + j];
+        const int qi = (int)udiv((uint32_t)(r0 + r), a.group_div);
+        const int64_t qrow = ((int64_t)b * a.q_len + qi) * a.n_heads + kvh * a.group +
+                             (r0 + r - qi * a.group);
+        if (a.n_chunks == 1) {
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            u32x4_t v;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                v[j] = (uint32_t)bf16_rne(o[2 * j] * inv) |
+                       (uint32_t)bf16_rne(o[2 * j + 1] * inv) << 16;
+            *reinterpret_cast<u32x4_t *>(a.out + qrow * D + d) = v;
+            if (a.lse && d == 0)
+                a.lse[qrow] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * LN2
+                                         : -__builtin_inff();
+        } else {
+            const int64_t pr = qrow * a.n_chunks + chunk;
+            if (d == 0) {
+                a.part_ml[2 * pr] = m;
+                a.part_ml[2 * pr + 1] = sum;
+            }
+            if (sum > 0.0f)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + d + 4 * h) =
+                        f32x4_t{o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]};
+        }
+    }
+}
+
+// Joins the chunks of one row per wavefront: sum_c 2^(m_c - m) O_c / sum.
+template <int D>
+__global__ void __launch_bounds__(256) nvfp4_attention_join_kernel(
+    const float *part_ml, const float *part_o, int n_chunks, int64_t n_rows, uint16_t *out,
+    float *lse)
+{
+    const int64_t row = (int64_t)wg_id() * 4 + wave_in_group();
+    if (row >= n_rows)
+        return;
+    constexpr int V = D / 64;
+    const int lane = (int)lane_id();
+    const float *ml = part_ml + 2 * row * n_chunks;
+    float m = NO_MAX;
+    for (int c = lane; c < n_chunks; c += 64)
+        m = __builtin_fmaxf(m, ml[2 * c + 1] > 0.0f ? ml[2 * c] : NO_MAX);
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1)
+        m = __builtin_fmaxf(m, lane_get(m, (uint32_t)(lane ^ k)));
+    float sum = 0.0f, o[V] = {};
+    for (int c = 0; c < n_chunks; c++) {
+        const float lc = ml[2 * c + 1];
+        if (lc > 0.0f) {
+            const float f = __builtin_amdgcn_exp2f(ml[2 * c] - m);
+            sum = __builtin_fmaf(lc, f, sum);
+#pragma unroll
+            for (int j = 0; j < V; j++)
+                o[j] = __builtin_fmaf(part_o[(row * n_chunks + c) * D + 64 * j + lane], f, o[j]);
+        }
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int j = 0; j < V; j++)
-        a.out[id * D + lane * V + j] = bf16_rne(o[j] * r);
-    if (a.lse && lane == 0)
-        a.lse[id] = l > 0.0f ? m + __builtin_amdgcn_logf(l) * LN2 : -__builtin_inff();
+        out[row * D + 64 * j + lane] = bf16_rne(o[j] * inv);
+    if (lse && lane == 0)
+        lse[row] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * LN2 : -__builtin_inff();
+}
+
+// Row tiles and key chunks of a launch.
+struct AttnPlan {
+    int rt, row_tiles, chunk, n_chunks;
+};
+AttnPlan attention_plan(int64_t n_seqs, int64_t q_len, int64_t n_heads, int64_t n_kv_heads,
+                        int64_t head_dim, int64_t max_keys)
+{
+    const int64_t rows = q_len * (n_heads / n_kv_heads);
+    // 64 rows of 128 or more elements do not fit a wavefront's registers.
+    const int rt = rows <= 16 ? 1 : rows <= 32 || head_dim > 64 ? 2 : 4;
+    const int64_t row_tiles = (rows + 16 * rt - 1) / (16 * rt);
+    const int64_t base = n_seqs * n_kv_heads * row_tiles;
+    int64_t n = (ATT_TARGET_WGS + base - 1) / base;
+    const int64_t most = (max_keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
+    n = n < 1 ? 1 : n > most ? most : n;
+    const int64_t step = ATT_TILE * ATT_WAVES;
+    const int64_t chunk = ((max_keys + n - 1) / n + step - 1) / step * step;
+    // A window moves the first key down to a multiple of the tile: one more chunk at most.
+    n = (max_keys + chunk - 1) / chunk;
+    return AttnPlan{rt, (int)row_tiles, (int)chunk, (int)n};
 }
 
 }  // namespace
 
-int64_t nvfp4_attention_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t)
+int64_t nvfp4_attention_workspace(int64_t n_seqs, int64_t q_len, int64_t n_heads,
+                                  int64_t n_kv_heads, int64_t head_dim, int64_t max_keys)
 {
-    return 0;
+    const AttnPlan p = attention_plan(n_seqs, q_len, n_heads, n_kv_heads, head_dim, max_keys);
+    if (p.n_chunks == 1)
+        return 0;
+    const int64_t parts = n_seqs * q_len * n_heads * p.n_chunks;
+    return (parts * 2 * 4 + 15) / 16 * 16 + parts * head_dim * 4;
 }
 
-hipError_t launch_nvfp4_attention(const AttnArgs &a, void *, hipStream_t stream)
+template <int D, int RT>
+static void attention_launch(const AttnK &k, int64_t wgs, hipStream_t stream)
 {
-    const dim3 grid((unsigned)(a.n_seqs * a.q_len * a.n_heads)), block(64);
+    hipLaunchKernelGGL((nvfp4_attention_kernel<D, RT>), dim3((unsigned)wgs), dim3(ATT_THREADS), 0,
+                       stream, k);
+}
+
+hipError_t launch_nvfp4_attention(const AttnArgs &a, void *workspace, hipStream_t stream)
+{
+    const int64_t max_keys = a.max_pages * a.page_size;
+    const AttnPlan p = attention_plan(a.n_seqs, a.q_len, a.n_heads, a.n_kv_heads, a.head_dim,
+                                      max_keys);
+    const int64_t n_rows = a.n_seqs * a.q_len * a.n_heads;
+    const int64_t parts = n_rows * p.n_chunks;
+    float *ml = static_cast<float *>(workspace);
+    const int group = (int)(a.n_heads / a.n_kv_heads);
+    const AttnK k{a.q, a.k, a.kbs, a.ks, a.v, a.vbs, a.vs, a.block_table, a.seq_lens, a.n_pages,
+                  a.max_pages, (int)a.q_len, (int)a.n_heads, (int)a.n_kv_heads, group,
+                  (int)a.page_size, (int)(a.q_len * group), make_div((uint32_t)a.page_size),
+                  make_div((uint32_t)group), a.scale * LOG2E, a.causal ? 1 : 0,
+                  (int)(a.window < 0x7FFFFFFF ? a.window : 0x7FFFFFFF), p.chunk, p.n_chunks,
+                  p.row_tiles, a.out, a.lse, ml, ml ? ml + (parts * 2 + 3) / 4 * 4 : nullptr};
+    const int64_t wgs = a.n_seqs * a.n_kv_heads * p.row_tiles * p.n_chunks;
     if (a.head_dim == 64)
-        hipLaunchKernelGGL(nvfp4_attention_kernel<64>, grid, block, 0, stream, a);
+        p.rt == 1 ? attention_launch<64, 1>(k, wgs, stream)
+        : p.rt == 2 ? attention_launch<64, 2>(k, wgs, stream)
+                    : attention_launch<64, 4>(k, wgs, stream);
     else if (a.head_dim == 128)
-        hipLaunchKernelGGL(nvfp4_attention_kernel<128>, grid, block, 0, stream, a);
+        p.rt == 1 ? attention_launch<128, 1>(k, wgs, stream)
+                  : attention_launch<128, 2>(k, wgs, stream);
     else
-        hipLaunchKernelGGL(nvfp4_attention_kernel<256>, grid, block, 0, stream, a);
+        p.rt == 1 ? attention_launch<256, 1>(k, wgs, stream)
+                  : attention_launch<256, 2>(k, wgs, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.n_chunks == 1)
+        return e;
+    const dim3 grid((unsigned)((n_rows + 3) / 4)), block(256);
+    auto join = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, stream, k.part_ml, k.part_o, p.n_chunks, n_rows,
+                           a.out, a.lse);
+    };
+    if (a.head_dim == 64)
+        join(nvfp4_attention_join_kernel<64>);
+    else if (a.head_dim == 128)
+        join(nvfp4_attention_join_kernel<128>);
+    else
+        join(nvfp4_attention_join_kernel<256>);
     return hipGetLastError();
 }
 
