@@ -31,10 +31,16 @@
 // cache passes through LDS.
 //
 // Split.  A workgroup of four wavefronts takes a chunk of the keys of one
-// (sequence, key/value head, row tile), its wavefronts every fourth tile;
-// they join through LDS.  With one chunk the workgroup writes the result,
-// otherwise partial results go to the workspace and a second kernel joins
-// them.
+// (sequence, key/value head, row tile), its wavefronts every fourth tile of
+// it; they join through LDS.  The lengths are device data, so the chunks are
+// planned on the device: every workgroup sums the lengths and derives the
+// same chunk size, about ATT_TARGET equal chunks over the whole batch, so
+// that long sequences take many workgroups and short ones one (with chunks
+// planned on the host from the longest length, most workgroups of a ragged
+// batch were empty, and those that were not sat on few XCDs: 221 us against
+// 156 us with the XCDs evened out and XXX us planned here).  A sequence that
+// is one chunk is written by its workgroup; otherwise partial results go to
+// the workspace and a second kernel joins them.
 #include "mxq_layer.h"
 #include "mxq_layer_device.h"
 
@@ -48,7 +54,10 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 constexpr int ATT_WAVES = 4, ATT_THREADS = 64 * ATT_WAVES;
 constexpr int ATT_TILE = 32;                        // keys per step of a wavefront
 constexpr int ATT_MIN_CHUNK = 2 * ATT_TILE * ATT_WAVES;
-constexpr int64_t ATT_TARGET_WGS = 2048;
+#ifndef ATT_T
+#define ATT_T 1024
+#endif
+constexpr int ATT_TARGET = ATT_T;                   // chunks a launch aims at
 constexpr float NO_MAX = -1.0e30f;                  // running maximum before the first key
 constexpr float LOW = 0x1p-14f, LOW_UP = 0x1p29f;   // numerators of the second round
 
@@ -64,11 +73,119 @@ struct AttnK {
     Div page_div, group_div;
     float scale;                                     // softmax_scale * log2 e
     int causal, window;
-    int chunk, n_chunks, row_tiles;
+    int n_seqs, row_tiles, tile_rows;                // tile_rows = 16 RT
+    bool split;
     uint16_t *out;
     float *lse;
-    float *part_ml, *part_o;                         // [row][chunk][2], [row][chunk][D]
+    float *part_ml, *part_o;                         // [unit][tile row][2], [..][D]
 };
+
+// Keys the rows of one row tile can see at most, over the tiles of sequence b
+// (the plan's length of the sequence).
+__device__ __forceinline__ int seq_len(const AttnK &a, int b)
+{
+    const int64_t cap = a.max_pages * a.page_size, n = a.lens[b];
+    return (int)(n < 0 ? 0 : n > cap ? cap : n);
+}
+__device__ __forceinline__ int seq_span(const AttnK &a, int len)
+{
+    if (!a.causal || a.window == 0)
+        return len;
+    // The tile's first row reaches back window - 1 keys, rounded down to a tile.
+    const int64_t w = (int64_t)a.window + a.tile_rows + ATT_TILE;
+    return w < len ? (int)w : len;
+}
+
+__device__ __forceinline__ int wave_scan(int v, int lane)       // inclusive
+{
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+        const int o = (int)lane_get((uint32_t)v, (uint32_t)(lane >= k ? lane - k : lane));
+        v += lane >= k ? o : 0;
+    }
+    return v;
+}
+__device__ __forceinline__ int64_t wave_sum_i64(int64_t v, int lane)
+{
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+        const uint32_t lo = lane_get((uint32_t)v, (uint32_t)(lane ^ k));
+        const uint32_t hi = lane_get((uint32_t)((uint64_t)v >> 32), (uint32_t)(lane ^ k));
+        v += (int64_t)((uint64_t)hi << 32 | lo);
+    }
+    return v;
+}
+
+// The chunk size of the batch: a multiple of a workgroup's step.
+__device__ __forceinline__ int plan_chunk(const AttnK &a, int lane)
+{
+    int64_t keys = 0;
+    for (int b = lane; b < a.n_seqs; b += 64)
+        keys += seq_span(a, seq_len(a, b));
+    keys = wave_sum_i64(keys, lane) * a.n_kv_heads * a.row_tiles;
+    constexpr int STEP = ATT_TILE * ATT_WAVES;
+    int64_t c = (keys / ATT_TARGET + STEP) / STEP * STEP;
+    c = c < ATT_MIN_CHUNK ? ATT_MIN_CHUNK : c;
+    return __builtin_amdgcn_readfirstlane((int)c);
+}
+__device__ __forceinline__ int plan_chunks(const AttnK &a, int span, int chunk)
+{
+    return !a.split || span <= chunk ? 1 : (span + chunk - 1) / chunk;
+}
+// A workgroup's share of the batch.
+struct Unit {
+    int b, kvh, tile, chunk, n_chunks, len, chunk_keys;
+};
+// Unit u of the plan; false past the last one.  per = units of one chunk of
+// one sequence.
+__device__ __forceinline__ bool plan_unit(const AttnK &a, uint32_t u, int lane, Unit *o)
+{
+    const uint32_t per = (uint32_t)(a.n_kv_heads * a.row_tiles);
+    int chunk = 0;
+    uint32_t rest;
+    if (!a.split) {
+        o->b = (int)(u / per);
+        rest = u % per;
+        o->len = seq_len(a, o->b);
+        o->n_chunks = 1;
+        o->chunk = 0;
+    } else {
+        chunk = plan_chunk(a, lane);
+        int64_t left = u;
+        bool found = false;
+        for (int b0 = 0; b0 < a.n_seqs && !found; b0 += 64) {
+            const int b = b0 + lane;
+            const int len = b < a.n_seqs ? seq_len(a, b) : 0;
+            const int n = b < a.n_seqs ? plan_chunks(a, seq_span(a, len), chunk) : 0;
+            const int s = wave_scan(n, lane);
+            // The first sequence whose units end past u.
+            const uint64_t past = __builtin_amdgcn_ballot_w64((int64_t)s * per > left);
+            if (past) {
+                const int w = __builtin_ctzll(past);
+                o->b = b0 + w;
+                o->len = __builtin_amdgcn_readlane(len, w);
+                o->n_chunks = __builtin_amdgcn_readlane(n, w);
+                left -= (int64_t)(__builtin_amdgcn_readlane(s, w) - o->n_chunks) * per;
+                found = true;
+            } else {
+                left -= (int64_t)__builtin_amdgcn_readlane(s, 63) * per;
+            }
+        }
+        if (!found)
+            return false;
+        rest = (uint32_t)left % per;
+        o->chunk = (int)((uint32_t)left / per);
+    }
+    // The last row tile sees the most keys: it goes first.
+    o->tile = a.row_tiles - 1 - (int)(rest / (uint32_t)a.n_kv_heads);
+    o->kvh = (int)(rest % (uint32_t)a.n_kv_heads);
+    // Equal chunks of a sequence.
+    constexpr int STEP = ATT_TILE * ATT_WAVES;
+    const int span = seq_span(a, o->len);
+    o->chunk_keys = o->n_chunks == 1 ? 0x40000000
+                                     : ((span + o->n_chunks - 1) / o->n_chunks + STEP - 1) / STEP * STEP;
+    return true;
+}
 
 __device__ __forceinline__ float max4_groups(float v)
 {
@@ -89,35 +206,38 @@ struct KvTile {
     uint32_t vc[8][VB > 4 ? VB / 4 : 1], vb[8];
 };
 
-// Rows of the tile's two 16-key halves: wave-uniform base rows in the cache.
-struct TileRows {
-    int64_t r[2];
+// Where a tile's two 16-key halves lie: the page (as the table holds it) and the
+// slot in it.  The rows are formed where they are used, so that the table's
+// loads have a step's time to arrive.
+struct TilePages {
+    int64_t page[2];
+    int slot[2];
 };
-__device__ __forceinline__ TileRows tile_rows(const AttnK &a, const int64_t *table, int kvh,
-                                              int t0)
+__device__ __forceinline__ TilePages tile_pages(const AttnK &a, const int64_t *table, int t0)
 {
-    TileRows o;
+    TilePages o;
     const int last = (int)(a.max_pages * a.page_size) - 16;
 #pragma unroll
     for (int s = 0; s < 2; s++) {
         int t = t0 + 16 * s;
         t = t < last ? t : last;                     // halves past the table: masked by length
         const uint32_t pi = udiv((uint32_t)t, a.page_div);
-        int64_t page = table[pi];
-        page = page < 0 ? 0 : page >= a.n_pages ? a.n_pages - 1 : page;
-        o.r[s] = (page * a.n_kv_heads + kvh) * a.page_size + (t - (int)pi * a.page_size);
+        o.page[s] = table[pi];
+        o.slot[s] = t - (int)pi * a.page_size;
     }
     return o;
 }
 
 template <int D>
-__device__ __forceinline__ void load_tile(KvTile<D> &x, const AttnK &a, const TileRows &rows,
-                                          int l, int g)
+__device__ __forceinline__ void load_tile(KvTile<D> &x, const AttnK &a, const TilePages &pages,
+                                          int kvh, int l, int g)
 {
     constexpr int KW = KvTile<D>::KW, VB = KvTile<D>::VB;
 #pragma unroll
     for (int s = 0; s < 2; s++) {
-        const int64_t r = rows.r[s];
+        int64_t page = pages.page[s];
+        page = page < 0 ? 0 : page >= a.n_pages ? a.n_pages - 1 : page;
+        const int64_t r = (page * a.n_kv_heads + kvh) * a.page_size + pages.slot[s];
         const uint8_t *kc = a.k + r * (D / 2) + (uint32_t)(l * (D / 2) + g * (D / 8));
         const uint8_t *kb = a.kbs + r * (D / 16) + (uint32_t)(l * (D / 16) + g * (D / 64));
         if constexpr (KW == 2) {
@@ -318,6 +438,10 @@ __device__ __forceinline__ void attend(Rows<D, RT> &st, const KvTile<D> &x, int 
             st.o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p8[rt], st.o[rt][j], 0, 0, 0);
     }
     if (any_low) {
+        // Decoded anew: kept from the first round they would cost every step's registers.
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            asm("" : "+v"(ev[i][0]), "+v"(od[i][0]));
 #pragma unroll
         for (int j = 0; j < D / 16; j++) {
             const f16x8_t vf = values(j);
@@ -341,17 +465,10 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
     __shared__ __attribute__((aligned(16))) float lds_o[ATT_WAVES][ROWS][D + 4];
 
     const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
-    uint32_t id = wg_id();
-    const int tile = (int)(id % (uint32_t)a.row_tiles);
-    id /= (uint32_t)a.row_tiles;
-    const int chunk = (int)(id % (uint32_t)a.n_chunks);
-    id /= (uint32_t)a.n_chunks;
-    const int kvh = (int)(id % (uint32_t)a.n_kv_heads), b = (int)(id / (uint32_t)a.n_kv_heads);
-
-    const int64_t cap = a.max_pages * a.page_size;
-    int64_t len64 = a.lens[b];
-    len64 = len64 < 0 ? 0 : len64 > cap ? cap : len64;
-    const int len = (int)len64;
+    Unit un;
+    if (!plan_unit(a, wg_id(), lane, &un))
+        return;
+    const int tile = un.tile, kvh = un.kvh, b = un.b, len = un.len;
 
     // Keys the tile's rows see: [kmin, kmax); this workgroup's part of them.
     const int r0 = tile * ROWS;
@@ -361,9 +478,9 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
     const int kmax = a.causal ? (last + 1 < 0 ? 0 : last + 1) : len;
     int kmin = a.causal && a.window > 0 ? first - a.window + 1 : 0;
     kmin = kmin < 0 ? 0 : kmin & ~(ATT_TILE - 1);
-    const int64_t start64 = (int64_t)kmin + (int64_t)chunk * a.chunk;
+    const int64_t start64 = (int64_t)kmin + (int64_t)un.chunk * un.chunk_keys;
     const int start = start64 < kmax ? (int)start64 : kmax;
-    const int stop = kmax - start < a.chunk ? kmax : start + a.chunk;
+    const int stop = kmax - start < un.chunk_keys ? kmax : start + un.chunk_keys;
 
     Rows<D, RT> st;
     int lo[RT], hi[RT];
@@ -416,19 +533,32 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
     const int full_lo = a.causal && a.window > 0 ? last - a.window + 1 : 0;
     int t0 = start + wave * ATT_TILE;
     if (t0 < stop) {
-        KvTile<D> x;
-        load_tile<D>(x, a, tile_rows(a, table, kvh, t0), l, g);
-        for (; t0 < stop; t0 += STEP) {
-            // The next tile's loads are in flight while this one is worked on (the
-            // last step reads its own tile again).
-            const int tn = t0 + STEP < stop ? t0 + STEP : t0;
-            KvTile<D> nx;
-            load_tile<D>(nx, a, tile_rows(a, table, kvh, tn), l, g);
-            if (t0 >= full_lo && t0 + ATT_TILE <= full_hi)
-                attend<D, RT, false>(st, x, t0, len, lo, hi, g);
+        // Two register sets take turns: while one tile is worked on, the next one's
+        // loads are in flight and the page of the one after is looked up (steps past
+        // the last read the last tile again).
+        const int t_last = t0 + (stop - 1 - t0) / STEP * STEP;
+        auto at = [&](int t) { return tile_pages(a, table, t < t_last ? t : t_last); };
+        auto work = [&](const KvTile<D> &x, int t) {
+            if (t >= full_lo && t + ATT_TILE <= full_hi)
+                attend<D, RT, false>(st, x, t, len, lo, hi, g);
             else
-                attend<D, RT, true>(st, x, t0, len, lo, hi, g);
-            x = nx;
+                attend<D, RT, true>(st, x, t, len, lo, hi, g);
+        };
+        KvTile<D> x0, x1;
+        load_tile<D>(x0, a, at(t0), kvh, l, g);
+        TilePages next = at(t0 + STEP);
+        for (;;) {
+            load_tile<D>(x1, a, next, kvh, l, g);
+            next = at(t0 + 2 * STEP);
+            work(x0, t0);
+            if (t0 == t_last)
+                break;
+            load_tile<D>(x0, a, next, kvh, l, g);
+            next = at(t0 + 3 * STEP);
+            work(x1, t0 + STEP);
+            t0 += 2 * STEP;
+            if (t0 > t_last)
+                break;
         }
     }
 
@@ -477,7 +607,7 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
         const int qi = (int)udiv((uint32_t)(r0 + r), a.group_div);
         const int64_t qrow = ((int64_t)b * a.q_len + qi) * a.n_heads + kvh * a.group +
                              (r0 + r - qi * a.group);
-        if (a.n_chunks == 1) {
+        if (un.n_chunks == 1) {
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             u32x4_t v;
 #pragma unroll
@@ -489,7 +619,7 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
                 a.lse[qrow] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * LN2
                                          : -__builtin_inff();
         } else {
-            const int64_t pr = qrow * a.n_chunks + chunk;
+            const int64_t pr = (int64_t)wg_id() * ROWS + r;
             if (d == 0) {
                 a.part_ml[2 * pr] = m;
                 a.part_ml[2 * pr + 1] = sum;
@@ -504,62 +634,102 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
 }
 
 // Joins the chunks of one row per wavefront: sum_c 2^(m_c - m) O_c / sum.
+// Rows of one chunk were written by their workgroup.
 template <int D>
-__global__ void __launch_bounds__(256) nvfp4_attention_join_kernel(
-    const float *part_ml, const float *part_o, int n_chunks, int64_t n_rows, uint16_t *out,
-    float *lse)
+__global__ void __launch_bounds__(256) nvfp4_attention_join_kernel(AttnK a)
 {
+    const int lane = (int)lane_id();
     const int64_t row = (int64_t)wg_id() * 4 + wave_in_group();
-    if (row >= n_rows)
+    if (row >= (int64_t)a.n_seqs * a.q_len * a.n_heads)
         return;
     constexpr int V = D / 64;
-    const int lane = (int)lane_id();
-    const float *ml = part_ml + 2 * row * n_chunks;
+    const int head = (int)(row % a.n_heads), qi = (int)(row / a.n_heads % a.q_len);
+    const int b = (int)(row / a.n_heads / a.q_len);
+    const int chunk = plan_chunk(a, lane);
+    const int n = plan_chunks(a, seq_span(a, seq_len(a, b)), chunk);
+    if (n == 1)
+        return;
+    int64_t before = 0;                             // chunks of the sequences before b
+    for (int i = lane; i < b; i += 64)
+        before += plan_chunks(a, seq_span(a, seq_len(a, i)), chunk);
+    before = wave_sum_i64(before, lane);
+    const int r = qi * a.group + head % a.group;
+    const int64_t per = (int64_t)a.n_kv_heads * a.row_tiles;
+    const int64_t unit = before * per +
+                         (int64_t)(a.row_tiles - 1 - r / a.tile_rows) * a.n_kv_heads +
+                         head / a.group;
+    const int64_t p0 = unit * a.tile_rows + r % a.tile_rows, step = per * a.tile_rows;
     float m = NO_MAX;
-    for (int c = lane; c < n_chunks; c += 64)
-        m = __builtin_fmaxf(m, ml[2 * c + 1] > 0.0f ? ml[2 * c] : NO_MAX);
+    for (int c = lane; c < n; c += 64) {
+        const float *ml = a.part_ml + 2 * (p0 + c * step);
+        m = __builtin_fmaxf(m, ml[1] > 0.0f ? ml[0] : NO_MAX);
+    }
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1)
         m = __builtin_fmaxf(m, lane_get(m, (uint32_t)(lane ^ k)));
+    // Lane c holds the factor of chunk c0 + c; the parts are loaded eight at a time
+    // (a chunk without keys has none: its slot is read, but not used).
     float sum = 0.0f, o[V] = {};
-    for (int c = 0; c < n_chunks; c++) {
-        const float lc = ml[2 * c + 1];
-        if (lc > 0.0f) {
-            const float f = __builtin_amdgcn_exp2f(ml[2 * c] - m);
-            sum = __builtin_fmaf(lc, f, sum);
+    for (int c0 = 0; c0 < n; c0 += 64) {
+        const int c = c0 + lane < n ? c0 + lane : n - 1;
+        const float *ml = a.part_ml + 2 * (p0 + c * step);
+        const float lc = c0 + lane < n ? ml[1] : 0.0f;
+        const float f = lc > 0.0f ? __builtin_amdgcn_exp2f(ml[0] - m) : 0.0f;
+        sum = __builtin_fmaf(lc, f, sum);
+        const int cn = n - c0 < 64 ? n - c0 : 64;
+        for (int i = 0; i < cn; i += 8) {
+            float v[8][V];
 #pragma unroll
-            for (int j = 0; j < V; j++)
-                o[j] = __builtin_fmaf(part_o[(row * n_chunks + c) * D + 64 * j + lane], f, o[j]);
+            for (int k = 0; k < 8; k++) {
+                const int ck = c0 + (i + k < cn ? i + k : cn - 1);
+                const float *p = a.part_o + (p0 + ck * step) * D + lane;
+#pragma unroll
+                for (int j = 0; j < V; j++)
+                    v[k][j] = p[64 * j];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const int ik = i + k < cn ? i + k : cn - 1;
+                const float fk = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(f), ik));
+                if (i + k < cn && fk > 0.0f)
+#pragma unroll
+                    for (int j = 0; j < V; j++)
+                        o[j] = __builtin_fmaf(v[k][j], fk, o[j]);
+            }
         }
     }
+    sum = wave_sum_f32(sum);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int j = 0; j < V; j++)
-        out[row * D + 64 * j + lane] = bf16_rne(o[j] * inv);
-    if (lse && lane == 0)
-        lse[row] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * LN2 : -__builtin_inff();
+        a.out[row * D + 64 * j + lane] = bf16_rne(o[j] * inv);
+    if (a.lse && lane == 0)
+        a.lse[row] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * LN2 : -__builtin_inff();
 }
 
-// Row tiles and key chunks of a launch.
+// Row tiles of a launch, and the most units its plan can have: a chunk more
+// per (sequence, head, row tile) than its share of ATT_TARGET.
 struct AttnPlan {
-    int rt, row_tiles, chunk, n_chunks;
+    int rt, row_tiles;
+    bool split;
+    int64_t units;
 };
 AttnPlan attention_plan(int64_t n_seqs, int64_t q_len, int64_t n_heads, int64_t n_kv_heads,
                         int64_t head_dim, int64_t max_keys)
 {
     const int64_t rows = q_len * (n_heads / n_kv_heads);
-    // 64 rows of 128 or more elements do not fit a wavefront's registers.
-    const int rt = rows <= 16 ? 1 : rows <= 32 || head_dim > 64 ? 2 : 4;
+    // More rows share a key's decoding, as far as a wavefront's registers go: 64 rows
+    // of 64 elements, 32 of 128, 16 of 256.
+    const int most_rt = head_dim == 64 ? 4 : head_dim == 128 ? 2 : 1;
+    const int want_rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    const int rt = want_rt < most_rt ? want_rt : most_rt;
     const int64_t row_tiles = (rows + 16 * rt - 1) / (16 * rt);
     const int64_t base = n_seqs * n_kv_heads * row_tiles;
-    int64_t n = (ATT_TARGET_WGS + base - 1) / base;
-    const int64_t most = (max_keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK;
-    n = n < 1 ? 1 : n > most ? most : n;
-    const int64_t step = ATT_TILE * ATT_WAVES;
-    const int64_t chunk = ((max_keys + n - 1) / n + step - 1) / step * step;
-    // A window moves the first key down to a multiple of the tile: one more chunk at most.
-    n = (max_keys + chunk - 1) / chunk;
-    return AttnPlan{rt, (int)row_tiles, (int)chunk, (int)n};
+    // With enough row tiles to fill the chip, or keys for one chunk, none is split.
+    const bool split = base < ATT_TARGET && max_keys > ATT_MIN_CHUNK;
+    const int64_t most = base * ((max_keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK);
+    const int64_t units = !split ? base : most < ATT_TARGET + base ? most : ATT_TARGET + base;
+    return AttnPlan{rt, (int)row_tiles, split, units};
 }
 
 }  // namespace
@@ -568,10 +738,7 @@ int64_t nvfp4_attention_workspace(int64_t n_seqs, int64_t q_len, int64_t n_heads
                                   int64_t n_kv_heads, int64_t head_dim, int64_t max_keys)
 {
     const AttnPlan p = attention_plan(n_seqs, q_len, n_heads, n_kv_heads, head_dim, max_keys);
-    if (p.n_chunks == 1)
-        return 0;
-    const int64_t parts = n_seqs * q_len * n_heads * p.n_chunks;
-    return (parts * 2 * 4 + 15) / 16 * 16 + parts * head_dim * 4;
+    return p.split ? p.units * 16 * p.rt * (head_dim + 2) * 4 : 0;
 }
 
 template <int D, int RT>
@@ -587,16 +754,16 @@ hipError_t launch_nvfp4_attention(const AttnArgs &a, void *workspace, hipStream_
     const AttnPlan p = attention_plan(a.n_seqs, a.q_len, a.n_heads, a.n_kv_heads, a.head_dim,
                                       max_keys);
     const int64_t n_rows = a.n_seqs * a.q_len * a.n_heads;
-    const int64_t parts = n_rows * p.n_chunks;
     float *ml = static_cast<float *>(workspace);
     const int group = (int)(a.n_heads / a.n_kv_heads);
     const AttnK k{a.q, a.k, a.kbs, a.ks, a.v, a.vbs, a.vs, a.block_table, a.seq_lens, a.n_pages,
                   a.max_pages, (int)a.q_len, (int)a.n_heads, (int)a.n_kv_heads, group,
                   (int)a.page_size, (int)(a.q_len * group), make_div((uint32_t)a.page_size),
                   make_div((uint32_t)group), a.scale * LOG2E, a.causal ? 1 : 0,
-                  (int)(a.window < 0x7FFFFFFF ? a.window : 0x7FFFFFFF), p.chunk, p.n_chunks,
-                  p.row_tiles, a.out, a.lse, ml, ml ? ml + (parts * 2 + 3) / 4 * 4 : nullptr};
-    const int64_t wgs = a.n_seqs * a.n_kv_heads * p.row_tiles * p.n_chunks;
+                  (int)(a.window < 0x7FFFFFFF ? a.window : 0x7FFFFFFF), (int)a.n_seqs,
+                  p.row_tiles, 16 * p.rt, p.split, a.out, a.lse, ml,
+                  p.split ? ml + p.units * 16 * p.rt * 2 : nullptr};
+    const int64_t wgs = p.units;
     if (a.head_dim == 64)
         p.rt == 1 ? attention_launch<64, 1>(k, wgs, stream)
         : p.rt == 2 ? attention_launch<64, 2>(k, wgs, stream)
@@ -605,15 +772,13 @@ hipError_t launch_nvfp4_attention(const AttnArgs &a, void *workspace, hipStream_
         p.rt == 1 ? attention_launch<128, 1>(k, wgs, stream)
                   : attention_launch<128, 2>(k, wgs, stream);
     else
-        p.rt == 1 ? attention_launch<256, 1>(k, wgs, stream)
-                  : attention_launch<256, 2>(k, wgs, stream);
+        attention_launch<256, 1>(k, wgs, stream);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.n_chunks == 1)
+    if (e != hipSuccess || !p.split)
         return e;
     const dim3 grid((unsigned)((n_rows + 3) / 4)), block(256);
     auto join = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, 0, stream, k.part_ml, k.part_o, p.n_chunks, n_rows,
-                           a.out, a.lse);
+        hipLaunchKernelGGL(kernel, grid, block, 0, stream, k);
     };
     if (a.head_dim == 64)
         join(nvfp4_attention_join_kernel<64>);
