@@ -780,10 +780,12 @@ typedef struct {
  *   workspace: mxq_nvfp4_attention_workspace(...) bytes.
  *   n_seqs * q_len * n_heads <= 2^25, max_pages * page_size <= 2^30, cache rows
  *   <= 2^40.
- * Scores, the running maximum and sum and the output are fp32; q is held in FP16 under
- * a power-of-two scale per row (as BF16 activations above) and the softmax's
- * numerators in FP16 (2^-11 relative) under the running maximum of their
- * products with the values' FP32 scales.
+ * Scores, the running maximum and sum and the output are fp32; q is held in
+ * FP16 under a power-of-two scale per row (as BF16 activations above) and the
+ * softmax's numerators, times the values' FP32 scales, in FP16 (2^-11
+ * relative) down to 2^-54 of the row's largest.  A value row whose FP32 scale is below
+ * 2^-100 counts as zeros; the others of a sequence must lie within 2^100 of
+ * each other.
  */
 int mxq_nvfp4_attention(const uint16_t *q, const mxq_nvfp4_cache *k, const mxq_nvfp4_cache *v,
                         const int64_t *block_table, const int64_t *seq_lens, int64_t n_seqs,

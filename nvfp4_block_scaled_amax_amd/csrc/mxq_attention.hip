@@ -14,21 +14,26 @@
 // for j < 4, of its second 16 otherwise).
 //   dec(code) dec(block scale) is an exact FP16 value (6 significant bits).
 // The FP32 scales stay out of the products: a key's scale multiplies its
-// scores, a value's scale multiplies the softmax's numerators p, which are
-// rounded to FP16 as p s_v 2^(14-E), with E the exponent of the running
-// maximum of p s_v, tracked beside the running maximum of the scores: the
-// largest numerator lands in [2^14, 2^15), and one within 2^-28 of it keeps
-// all its 11 bits whatever the scales are.  A step with smaller ones (whose
-// values may be all that an output element is made of, where the others'
-// codes are 0) takes those in a second round of products under 2^29.  q is exact in FP16 under a
-// power of two per row.
+// scores, and a value's scale s_v goes into the softmax's exponent, so that
+// the numerators are 2^(z + log2 s_v - m + TOP), m the running maximum of
+// z + log2 s_v (to within SLACK).  They are rounded to FP16: the largest is
+// 2^11 to 2^15, and one within 2^-25 of it keeps all its 11 bits whatever
+// the scales are.  A step with smaller ones (whose values may be all that an output element is made
+// of, where the others' codes are 0) takes those in a second round of
+// products under 2^29.  The sum takes each numerator times 1 / s_v.  q is
+// exact in FP16 under a power of two per row.
 //   Operand order.  A lane reads the D/4 consecutive elements of a key that
-// belong to its group (one 16-byte load at D = 128) and the queries are
-// loaded in the same order.  Of a value row lane l reads elements D/16 l
-// onwards; two keys' nibbles are merged byte-wise (even and odd elements),
-// so that one conversion yields the pair (key t, key t + 1) of one element,
-// which is what the second product's first operand holds.  Nothing of the
-// cache passes through LDS.
+// belong to its group (16 bytes at D = 128) and the queries are loaded in the
+// same order.  Of a value row lane l reads elements D/16 l onwards; two keys'
+// nibbles are merged byte-wise (even and odd elements), so that one
+// conversion yields the pair (key t, key t + 1) of one element, which is what
+// the second product's first operand holds.
+//
+// Pipeline.  A wavefront copies its tiles straight into LDS
+// (global_load_lds, which needs no registers), ATT_STAGES tiles deep, and
+// waits for its own copies by count; nothing is shared between wavefronts,
+// so there is no barrier in the loop.  (Tiles in registers, one ahead: 44
+// loads a tile instead of 7, and 90 registers more.)
 //
 // Split.  A workgroup of four wavefronts takes a chunk of the keys of one
 // (sequence, key/value head, row tile), its wavefronts every fourth tile of
@@ -38,9 +43,11 @@
 // that long sequences take many workgroups and short ones one (with chunks
 // planned on the host from the longest length, most workgroups of a ragged
 // batch were empty, and those that were not sat on few XCDs: 221 us against
-// 156 us with the XCDs evened out and XXX us planned here).  A sequence that
+// 156 us with the XCDs evened out, 71 us planned here).  A sequence that
 // is one chunk is written by its workgroup; otherwise partial results go to
 // the workspace and a second kernel joins them.
+#include <type_traits>
+
 #include "mxq_layer.h"
 #include "mxq_layer_device.h"
 
@@ -54,12 +61,13 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 constexpr int ATT_WAVES = 4, ATT_THREADS = 64 * ATT_WAVES;
 constexpr int ATT_TILE = 32;                        // keys per step of a wavefront
 constexpr int ATT_MIN_CHUNK = 2 * ATT_TILE * ATT_WAVES;
-#ifndef ATT_T
-#define ATT_T 1024
-#endif
-constexpr int ATT_TARGET = ATT_T;                   // chunks a launch aims at
+constexpr int ATT_TARGET = 640;                    // chunks a launch aims at
 constexpr float NO_MAX = -1.0e30f;                  // running maximum before the first key
-constexpr float LOW = 0x1p-14f, LOW_UP = 0x1p29f;   // numerators of the second round
+constexpr float TOP = 11.0f, SLACK = 4.0f;          // numerators: 2^TOP at m, 2^15 at m + SLACK
+constexpr float LOW_LOG2 = -14.0f, LOW = 0x1p-14f;  // smaller ones go to the second round,
+constexpr float LOW_UP = 0x1p29f;                   // under this factor
+constexpr float MIN_VS = 0x1p-100f;                 // value scales below count as 0
+constexpr int ATT_STAGES = 2;                      // tiles in LDS per wavefront
 
 struct AttnK {
     const uint16_t *q;
@@ -196,92 +204,129 @@ __device__ __forceinline__ float max4_groups(float v)
 }
 __device__ __forceinline__ float sum4_groups(float v) { return sum32_f32(sum16_f32(v)); }
 
-// One tile's cache data of a lane.
-template <int D>
-struct KvTile {
-    static constexpr int KW = D / 32;                // dwords of a key's codes per lane
-    static constexpr int VB = D / 32;                // bytes of a value's codes per lane
-    uint32_t kc[2][KW], kb[2];
-    f32x4_t ks[2], vs[2];
-    uint32_t vc[8][VB > 4 ? VB / 4 : 1], vb[8];
+// The cache rows of a tile's two 16-key halves (their first keys; a half lies
+// in one page, so its 16 rows are consecutive).
+struct TileRows {
+    int64_t r[2];
 };
-
-// Where a tile's two 16-key halves lie: the page (as the table holds it) and the
-// slot in it.  The rows are formed where they are used, so that the table's
-// loads have a step's time to arrive.
-struct TilePages {
-    int64_t page[2];
-    int slot[2];
+// Rows of a wavefront's next 64 tiles, one tile a lane.  Looked up tile by tile
+// with scalar loads, the page table cost every step a memory latency: LDS
+// reads wait for the same counter.
+struct RowWindow {
+    uint32_t lo[2], hi[2];
 };
-__device__ __forceinline__ TilePages tile_pages(const AttnK &a, const int64_t *table, int t0)
+__device__ __forceinline__ RowWindow row_window(const AttnK &a, const int64_t *table, int kvh,
+                                                int t0, int step, int t_last, int lane)
 {
-    TilePages o;
+    RowWindow w;
     const int last = (int)(a.max_pages * a.page_size) - 16;
+    // Tiles past the wavefront's last stand for it.
+    const int n = (t_last - t0) / step;
+    const int tile = t0 + (lane < n ? lane : n) * step;
 #pragma unroll
     for (int s = 0; s < 2; s++) {
-        int t = t0 + 16 * s;
+        int t = tile + 16 * s;
         t = t < last ? t : last;                     // halves past the table: masked by length
         const uint32_t pi = udiv((uint32_t)t, a.page_div);
-        o.page[s] = table[pi];
-        o.slot[s] = t - (int)pi * a.page_size;
+        int64_t page = table[pi];
+        page = page < 0 ? 0 : page >= a.n_pages ? a.n_pages - 1 : page;
+        const int64_t r = (page * a.n_kv_heads + kvh) * a.page_size + (t - (int)pi * a.page_size);
+        w.lo[s] = (uint32_t)r;
+        w.hi[s] = (uint32_t)((uint64_t)r >> 32);
     }
+    return w;
+}
+__device__ __forceinline__ TileRows window_rows(const RowWindow &w, int i)
+{
+    TileRows o;
+#pragma unroll
+    for (int s = 0; s < 2; s++)
+        o.r[s] = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)w.hi[s], i) << 32 |
+                           (uint32_t)__builtin_amdgcn_readlane((int)w.lo[s], i));
     return o;
 }
 
+// A tile in LDS: codes of the 32 keys, codes of the values, block scales of
+// both, and the FP32 scales (keys, then values).
 template <int D>
-__device__ __forceinline__ void load_tile(KvTile<D> &x, const AttnK &a, const TilePages &pages,
-                                          int kvh, int l, int g)
+struct Stage {
+    static constexpr int CODES = 32 * (D / 2), BLOCKS = 32 * (D / 16);
+    static constexpr int BLOCK_ROOM = BLOCKS < 256 ? 256 : BLOCKS;     // whole 64-lane copies
+    static constexpr int K = 0, V = CODES, KB = 2 * CODES, VB = KB + BLOCK_ROOM,
+                         S = VB + BLOCK_ROOM, BYTES = S + 256;
+    static constexpr int COPIES = 2 * (CODES / 1024) + 2 * (BLOCK_ROOM / 256) + 1;
+};
+
+// Copies of 16 or 4 bytes a lane from per-lane addresses to LDS bytes lds + 16 lane
+// (4 lane).  The compiler does not track them: the loop counts them.
+__device__ __forceinline__ void to_lds16(const uint8_t *p, uint32_t lds)
 {
-    constexpr int KW = KvTile<D>::KW, VB = KvTile<D>::VB;
-#pragma unroll
-    for (int s = 0; s < 2; s++) {
-        int64_t page = pages.page[s];
-        page = page < 0 ? 0 : page >= a.n_pages ? a.n_pages - 1 : page;
-        const int64_t r = (page * a.n_kv_heads + kvh) * a.page_size + pages.slot[s];
-        const uint8_t *kc = a.k + r * (D / 2) + (uint32_t)(l * (D / 2) + g * (D / 8));
-        const uint8_t *kb = a.kbs + r * (D / 16) + (uint32_t)(l * (D / 16) + g * (D / 64));
-        if constexpr (KW == 2) {
-            const uint2 c = ld8(kc);
-            x.kc[s][0] = c.x;
-            x.kc[s][1] = c.y;
-            x.kb[s] = *kb;
-        } else {
-#pragma unroll
-            for (int j = 0; j < KW / 4; j++) {
-                const uint4 c = ld16(kc + 16 * j);
-                x.kc[s][4 * j] = c.x;
-                x.kc[s][4 * j + 1] = c.y;
-                x.kc[s][4 * j + 2] = c.z;
-                x.kc[s][4 * j + 3] = c.w;
-            }
-            if constexpr (KW == 4)
-                x.kb[s] = *reinterpret_cast<const uint16_t *>(kb);
-            else
-                x.kb[s] = *reinterpret_cast<const uint32_t *>(kb);
-        }
-        x.ks[s] = *reinterpret_cast<const f32x4_t *>(a.ks + r + 4 * g);
-        x.vs[s] = *reinterpret_cast<const f32x4_t *>(a.vs + r + 4 * g);
-        const uint8_t *vc = a.v + r * (D / 2) + (uint32_t)(4 * g * (D / 2) + l * VB);
-        const uint8_t *vb = a.vbs + r * (D / 16) + (uint32_t)(4 * g * (D / 16) + l * (D / 16) / 16);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint8_t *p = vc + i * (D / 2);
-            if constexpr (VB == 2)
-                x.vc[4 * s + i][0] = *reinterpret_cast<const uint16_t *>(p);
-            else if constexpr (VB == 4)
-                x.vc[4 * s + i][0] = *reinterpret_cast<const uint32_t *>(p);
-            else {
-                const uint2 c = ld8(p);
-                x.vc[4 * s + i][0] = c.x;
-                x.vc[4 * s + i][1] = c.y;
-            }
-            x.vb[4 * s + i] = vb[i * (D / 16)];
-        }
-    }
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(p), "s"(lds)
+                 : "memory", "m0");
+}
+// The same from a wave-uniform base and a lane's offset.
+__device__ __forceinline__ void to_lds16(const uint8_t *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds4(const uint8_t *p, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off"
+                 :
+                 : "v"(p), "s"(lds)
+                 : "memory", "m0");
+}
+// Waits until at most N of the wavefront's copies are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_copies()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt field");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
-// E4M3 byte -> FP16 (exact).
-__device__ __forceinline__ _Float16 e4m3_f16(uint32_t byte) { return (_Float16)e4m3_value(byte); }
+template <int D>
+__device__ __forceinline__ void copy_tile(const AttnK &a, const TileRows &rows, uint32_t lds,
+                                          int lane)
+{
+    using St = Stage<D>;
+    // Byte i of a half's 16 rows is byte i from its first row.
+    constexpr int HALF = St::CODES / 2, BHALF = St::BLOCKS / 2;
+#pragma unroll
+    for (int c = 0; c < St::CODES / 1024; c++) {
+        if constexpr (HALF >= 1024) {
+            constexpr int PER = HALF / 1024;         // copies of a half
+            const int64_t r = rows.r[c / PER] * (D / 2) + 1024 * (c % PER);
+            to_lds16(a.k + r, (uint32_t)(16 * lane), lds + St::K + 1024 * c);
+            to_lds16(a.v + r, (uint32_t)(16 * lane), lds + St::V + 1024 * c);
+        } else {
+            const int64_t r = (lane & 32 ? rows.r[1] : rows.r[0]) * (D / 2) + 16 * (lane & 31);
+            to_lds16(a.k + r, lds + St::K);
+            to_lds16(a.v + r, lds + St::V);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < St::BLOCK_ROOM / 256; c++) {
+        // D = 64: the upper lanes read what the lower ones do.
+        const int at = (256 * c + 4 * lane) % St::BLOCKS;
+        const int64_t r = (at >= BHALF ? rows.r[1] : rows.r[0]) * (D / 16) + at % BHALF;
+        to_lds4(a.kbs + r, lds + St::KB + 256 * c);
+        to_lds4(a.vbs + r, lds + St::VB + 256 * c);
+    }
+    const int64_t r = (lane & 16 ? rows.r[1] : rows.r[0]) + (lane & 15);
+    to_lds4(reinterpret_cast<const uint8_t *>((lane & 32 ? a.vs : a.ks) + r), lds + St::S);
+}
+
+// Two E4M3 bytes -> FP16 (exact).
+__device__ __forceinline__ f16x2_t e4m3_pair_f16(uint32_t bytes)
+{
+    return __builtin_bit_cast(f16x2_t,
+                              __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(bytes, 1.0f, false));
+}
 
 template <int J>
 __device__ __forceinline__ f16x2_t pair_f16(uint32_t codes)
@@ -305,122 +350,147 @@ __device__ __forceinline__ f16x2_t pair_f16_dyn(uint32_t codes, int j)
 }
 
 // State of a wavefront's 16 RT rows.  Row (lane % 16) of tile rt: running
-// maximum m of the scores (log2 units), this lane's part of the sum l, the
-// running maximum w of p s_v relative to m, and O^T in units of 2^(e - 14).
+// maximum m of the numerators' exponents z + log2 s_v, this lane's part of
+// the sum l, and O^T; l and O in units of 2^(m - TOP).
 template <int D, int RT>
 struct Rows {
     f16x8_t q[RT][D / 32];
     float c[RT];                                     // score factor of the row
-    float m[RT], l[RT], w[RT];
-    int e[RT];
+    float m[RT], l[RT];
     f32x4_t o[RT][D / 16];
 };
 
-template <int D, int RT, bool MASKED>
-__device__ __forceinline__ void attend(Rows<D, RT> &st, const KvTile<D> &x, int t0, int len,
-                                       const int (&lo)[RT], const int (&hi)[RT], int g)
+// A lane's address in LDS, opaque, so that the accesses from it take their
+// constant distances as instruction offsets (else each is an addition).
+typedef __attribute__((address_space(3))) const uint8_t *lds_cptr;
+__device__ __forceinline__ lds_cptr lds_at(uint32_t address)
 {
+    asm("" : "+v"(address));
+    return (lds_cptr)(uintptr_t)address;
+}
+template <typename T>
+__device__ __forceinline__ T lds_ld(lds_cptr p)
+{
+    return *reinterpret_cast<__attribute__((address_space(3))) const T *>(p);
+}
+
+// One step: the tile at LDS address x (keys t0 ..).
+template <int D, int RT, bool MASKED>
+__device__ __forceinline__ void attend(Rows<D, RT> &st, uint32_t x, int t0, int len,
+                                       const int (&lo)[RT], const int (&hi)[RT], int l, int g)
+{
+    using St = Stage<D>;
     constexpr int KK = D / 32;
     // Scores: two 16-key halves, KK steps of 8 elements per lane group.
     f32x4_t s[2][RT];
 #pragma unroll
+    for (int rt = 0; rt < RT; rt++)
+        s[0][rt] = s[1][rt] = f32x4_t{};
+    uint32_t kc[2][KK], kb[2];
+    const lds_cptr pk = lds_at(x + St::K + l * (D / 2) + g * (D / 8));
+    const lds_cptr pkb = lds_at(x + St::KB + l * (D / 16) + g * (D / 64));
+#pragma unroll
     for (int h = 0; h < 2; h++) {
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++)
-            s[h][rt] = f32x4_t{};
-#pragma unroll
-        for (int kk = 0; kk < KK; kk++) {
-            // The D/4 elements of a lane hold D/64 blocks of 16 (two dwords each).
-            const _Float16 d = e4m3_f16((x.kb[h] >> (8 * (kk / 2))) & 0xFFu);
-            const f16x8_t kf = oct_f16(x.kc[h][kk], f16x2_t{d, d});
-#pragma unroll
-            for (int rt = 0; rt < RT; rt++)
-                s[h][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, st.q[rt][kk], s[h][rt], 0, 0,
-                                                                   0);
-        }
-    }
-    f32x4_t vs[2] = {x.vs[0], x.vs[1]};
-    if constexpr (MASKED) {
-        // Slots past the length may hold anything: their value scales count as 0.
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (t0 + 16 * (j >> 2) + 4 * g + (j & 3) >= len)
-                vs[j >> 2][j & 3] = 0.0f;
-    }
-    f16x8_t p8[RT], p8lo[RT];
-    bool any_low = false;
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        float z[8], tm = NO_MAX;
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            z[j] = s[j >> 2][rt][j & 3] * (x.ks[j >> 2][j & 3] * st.c[rt]);
-            if constexpr (MASKED) {
-                const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                z[j] = t >= lo[rt] && t < hi[rt] ? z[j] : NO_MAX;
-            }
-            tm = __builtin_fmaxf(tm, z[j]);
-        }
-        tm = max4_groups(tm);
-        const float mn = __builtin_fmaxf(st.m[rt], tm);
-        const float al = __builtin_amdgcn_exp2f(st.m[rt] - mn);
-        float sum = 0.0f, pw[8], wm = 0.0f, pm = 1.0e30f;
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            float p = __builtin_amdgcn_exp2f(z[j] - mn);
-            if constexpr (MASKED)
-                p = z[j] == NO_MAX ? 0.0f : p;
-            sum += p;
-            pw[j] = p * vs[j >> 2][j & 3];
-            wm = __builtin_fmaxf(wm, pw[j]);
-            pm = __builtin_fminf(pm, pw[j]);
-        }
-        wm = max4_groups(wm);
-        const float wn = __builtin_fmaxf(st.w[rt] * al, wm);
-        int e = (int)(f2u(wn) >> 23) - 127;
-        // Twelve binades above the smallest normal number: 2^(14 - e) stays finite.
-        e = e < -112 ? -112 : e;
-        const float up = u2f((uint32_t)(14 - e + 127) << 23);       // 2^(14 - e)
-        const float f = __builtin_ldexpf(al, st.e[rt] - e);
-        st.m[rt] = mn;
-        st.l[rt] = __builtin_fmaf(st.l[rt], al, sum);
-        st.w[rt] = wn;
-        st.e[rt] = e;
-#pragma unroll
-        for (int j = 0; j < D / 16; j++)
-            st.o[rt][j] *= f;
-        p8lo[rt] = f16x8_t{};
-        if (__builtin_amdgcn_ballot_w64(pm * up < LOW) != 0) {      // zeros too: harmless
-            any_low = true;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const float x = pw[j] * up;
-                p8lo[rt][j] = (_Float16)(x < LOW ? x * LOW_UP : 0.0f);
-                p8[rt][j] = (_Float16)(x < LOW ? 0.0f : x);
-            }
+        if constexpr (KK == 2) {
+            const u32x2_t c = lds_ld<u32x2_t>(pk + 16 * h * (D / 2));
+            kc[h][0] = c[0];
+            kc[h][1] = c[1];
+            kb[h] = lds_ld<uint8_t>(pkb + 16 * h * (D / 16));
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                p8[rt][j] = (_Float16)(pw[j] * up);
+            for (int j = 0; j < KK / 4; j++) {
+                const u32x4_t c = lds_ld<u32x4_t>(pk + 16 * h * (D / 2) + 16 * j);
+#pragma unroll
+                for (int w = 0; w < 4; w++)
+                    kc[h][4 * j + w] = c[w];
+            }
+            if constexpr (KK == 4)
+                kb[h] = lds_ld<uint16_t>(pkb + 16 * h * (D / 16));
+            else
+                kb[h] = lds_ld<uint32_t>(pkb + 16 * h * (D / 16));
         }
+    }
+#pragma unroll
+    for (int kk = 0; kk < KK; kk++) {
+        f16x8_t kf[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            // The D/4 elements of a lane hold D/64 blocks of 16 (two dwords each).
+            const f16x2_t d = e4m3_pair_f16(kb[h] >> (16 * (kk / 4)));
+            const _Float16 dk = d[(kk / 2) & 1];
+            kf[h] = oct_f16(kc[h][kk], f16x2_t{dk, dk});
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                s[h][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[h], st.q[rt][kk], s[h][rt],
+                                                                   0, 0, 0);
+    }
+    // The lane group's eight keys, and their values' codes and block scales.
+    const lds_cptr ps = lds_at(x + St::S + 16 * g);
+    const lds_cptr pv = lds_at(x + St::V + 4 * g * (D / 2) + l * (D / 32));
+    const lds_cptr pvb = lds_at(x + St::VB + 4 * g * (D / 16) + l * (D / 16) / 16);
+    constexpr int VW = D == 256 ? 2 : 1;             // dwords of a key's codes per lane
+    f32x4_t ks[2], vs[2];
+    uint32_t vc[8][VW], vb[8];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        ks[h] = lds_ld<f32x4_t>(ps + 64 * h);
+        vs[h] = lds_ld<f32x4_t>(ps + 128 + 64 * h);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const int key = 16 * (j >> 2) + (j & 3);
+        if constexpr (D == 64)
+            vc[j][0] = lds_ld<uint16_t>(pv + key * (D / 2));
+        else if constexpr (D == 128)
+            vc[j][0] = lds_ld<uint32_t>(pv + key * (D / 2));
+        else {
+            const u32x2_t w = lds_ld<u32x2_t>(pv + key * (D / 2));
+            vc[j][0] = w[0];
+            vc[j][1] = w[1];
+        }
+        vb[j] = lds_ld<uint8_t>(pvb + key * (D / 16));
+    }
+    // lv = log2 s_v, rv = 2^-lv.  A value scale of 0 (below MIN_VS) stands for a row of
+    // zeros, and slots past the length may hold anything: their block scales count
+    // as 0, and they take part in the sum under the largest scale beside them.
+    float lv[8], rv[8], vmin = vs[0][0];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        lv[j] = vs[j >> 2][j & 3];
+        vmin = __builtin_fminf(vmin, lv[j]);
+    }
+    if (MASKED || __builtin_amdgcn_ballot_w64(vmin < MIN_VS) != 0) {
+        float vz = MIN_VS;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const bool live = lv[j] >= MIN_VS && t0 + 16 * (j >> 2) + 4 * g + (j & 3) < len;
+            vb[j] = live ? vb[j] : 0;
+            lv[j] = live ? lv[j] : 0.0f;
+            vz = __builtin_fmaxf(vz, lv[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            lv[j] = lv[j] > 0.0f ? lv[j] : vz;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        lv[j] = __builtin_amdgcn_logf(lv[j]);
+        rv[j] = __builtin_amdgcn_exp2f(-lv[j]);
     }
     // Values: pairs of keys (2i, 2i + 1) of the lane group's eight.
     f16x2_t vd[4];
-    uint32_t ev[4][KvTile<D>::VB > 4 ? 2 : 1], od[4][KvTile<D>::VB > 4 ? 2 : 1];
+    uint32_t ev[4][VW], od[4][VW];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        uint32_t b0 = x.vb[2 * i], b1 = x.vb[2 * i + 1];
-        if constexpr (MASKED) {
-            const int t = t0 + 16 * (i >> 1) + 4 * g + 2 * (i & 1);
-            b0 = t < len ? b0 : 0;
-            b1 = t + 1 < len ? b1 : 0;
-        }
-        vd[i] = f16x2_t{e4m3_f16(b0), e4m3_f16(b1)};
+        vd[i] = e4m3_pair_f16(vb[2 * i] | vb[2 * i + 1] << 8);
 #pragma unroll
-        for (int wd = 0; wd < (KvTile<D>::VB > 4 ? 2 : 1); wd++) {
-            const uint32_t c0 = x.vc[2 * i][wd], c1 = x.vc[2 * i + 1][wd];
-            ev[i][wd] = (c0 & 0x0F0F0F0Fu) | ((c1 << 4) & 0xF0F0F0F0u);
-            od[i][wd] = ((c0 >> 4) & 0x0F0F0F0Fu) | (c1 & 0xF0F0F0F0u);
+        for (int w = 0; w < VW; w++) {
+            const uint32_t c0 = vc[2 * i][w], c1 = vc[2 * i + 1][w];
+            ev[i][w] = (c0 & 0x0F0F0F0Fu) | ((c1 << 4) & 0xF0F0F0F0u);
+            od[i][w] = ((c0 >> 4) & 0x0F0F0F0Fu) | (c1 & 0xF0F0F0F0u);
         }
     }
     auto values = [&](int j) {
@@ -430,39 +500,97 @@ __device__ __forceinline__ void attend(Rows<D, RT> &st, const KvTile<D> &x, int 
             v[i] = pair_f16_dyn((j & 1) ? od[i][j >> 3] : ev[i][j >> 3], (j >> 1) & 3) * vd[i];
         return cat8(v[0], v[1], v[2], v[3]);
     };
+    // The same, decoded anew where it is called: shared with the other uses, the
+    // decoded values would stay in registers.
+    auto values_again = [&](int j) {
+        f16x2_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            uint32_t c = (j & 1) ? od[i][j >> 3] : ev[i][j >> 3];
+            asm volatile("" : "+v"(c));
+            v[i] = pair_f16_dyn(c, (j >> 1) & 3) * vd[i];
+        }
+        return cat8(v[0], v[1], v[2], v[3]);
+    };
+    f16x8_t p8[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        float z[8], zx = NO_MAX, zn = -NO_MAX;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            z[j] = __builtin_fmaf(s[j >> 2][rt][j & 3], ks[j >> 2][j & 3] * st.c[rt], lv[j]);
+            if constexpr (MASKED) {
+                const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
+                z[j] = t >= lo[rt] && t < hi[rt] ? z[j] : NO_MAX;
+            }
+            zx = __builtin_fmaxf(zx, z[j]);
+            zn = __builtin_fminf(zn, z[j]);
+        }
+        // m follows the maximum only when that is past m + SLACK: with m exact, nearly
+        // every step of a short chunk had some row whose maximum rose.
+        zx = max4_groups(zx);
+        if (__builtin_amdgcn_ballot_w64(zx > st.m[rt] + SLACK) != 0) {
+            const float mn = zx > st.m[rt] + SLACK ? zx : st.m[rt];
+            const float al = __builtin_amdgcn_exp2f(st.m[rt] - mn);
+            st.m[rt] = mn;
+            st.l[rt] *= al;
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                st.o[rt][j] *= al;
+        }
+        const float base = st.m[rt] - TOP;
+        float p[8], sum[2] = {};
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            p[j] = __builtin_amdgcn_exp2f(z[j] - base);
+            if constexpr (MASKED)                    // a row that has seen no key: m = NO_MAX
+                p[j] = z[j] == NO_MAX ? 0.0f : p[j];
+            sum[j & 1] = __builtin_fmaf(p[j], rv[j], sum[j & 1]);
+        }
+        st.l[rt] += sum[0] + sum[1];
+        if (__builtin_amdgcn_ballot_w64(zn - base < LOW_LOG2) != 0) {   // masked keys too: harmless
+            f16x8_t plo;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                plo[j] = (_Float16)(p[j] < LOW ? p[j] * LOW_UP : 0.0f);
+                p[j] = p[j] < LOW ? 0.0f : p[j];
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; j++) {
+                const f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_f16(values_again(j), plo,
+                                                                         f32x4_t{}, 0, 0, 0);
+                st.o[rt][j] += o * (1.0f / LOW_UP);
+                __builtin_amdgcn_sched_barrier(0);   // one at a time: registers
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            p8[rt][j] = (_Float16)p[j];
+    }
 #pragma unroll
     for (int j = 0; j < D / 16; j++) {
         const f16x8_t vf = values(j);
 #pragma unroll
         for (int rt = 0; rt < RT; rt++)
             st.o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p8[rt], st.o[rt][j], 0, 0, 0);
-    }
-    if (any_low) {
-        // Decoded anew: kept from the first round they would cost every step's registers.
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            asm("" : "+v"(ev[i][0]), "+v"(od[i][0]));
-#pragma unroll
-        for (int j = 0; j < D / 16; j++) {
-            const f16x8_t vf = values(j);
-#pragma unroll
-            for (int rt = 0; rt < RT; rt++) {
-                const f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p8lo[rt], f32x4_t{},
-                                                                         0, 0, 0);
-                st.o[rt][j] += o * (1.0f / LOW_UP);
-            }
-        }
+        if (j & 1)
+            __builtin_amdgcn_sched_barrier(0);
     }
 }
 
 template <int D, int RT>
-__global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(ATT_THREADS, D * RT <= 128 ? 3 : 2)
     nvfp4_attention_kernel(AttnK a)
 {
     constexpr int ROWS = 16 * RT;
+    // The wavefronts' tiles; after the loop their sums: rows padded by four floats, so
+    // that the 16 rows a store touches miss each other's banks.
+    constexpr int TILE_BYTES = ATT_WAVES * ATT_STAGES * Stage<D>::BYTES;
+    constexpr int SUM_BYTES = ATT_WAVES * ROWS * (D + 4) * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t
+        lds[TILE_BYTES > SUM_BYTES ? TILE_BYTES : SUM_BYTES];
     __shared__ float lds_ml[ATT_WAVES][ROWS][2];
-    // Rows padded by four floats: the 16 rows a store touches miss each other's banks.
-    __shared__ __attribute__((aligned(16))) float lds_o[ATT_WAVES][ROWS][D + 4];
+    float(*lds_o)[ROWS][D + 4] = reinterpret_cast<float(*)[ROWS][D + 4]>(lds);
 
     const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
     Unit un;
@@ -519,8 +647,6 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
         }
         st.m[rt] = NO_MAX;
         st.l[rt] = 0.0f;
-        st.w[rt] = 0.0f;
-        st.e[rt] = -112;
 #pragma unroll
         for (int j = 0; j < D / 16; j++)
             st.o[rt][j] = f32x4_t{};
@@ -533,33 +659,44 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
     const int full_lo = a.causal && a.window > 0 ? last - a.window + 1 : 0;
     int t0 = start + wave * ATT_TILE;
     if (t0 < stop) {
-        // Two register sets take turns: while one tile is worked on, the next one's
-        // loads are in flight and the page of the one after is looked up (steps past
-        // the last read the last tile again).
+        // Tiles go round ATT_STAGES buffers.  Steps past the last copy the last tile
+        // again, so that the count of copies in flight is the same in every step.
+        using St = Stage<D>;
         const int t_last = t0 + (stop - 1 - t0) / STEP * STEP;
-        auto at = [&](int t) { return tile_pages(a, table, t < t_last ? t : t_last); };
-        auto work = [&](const KvTile<D> &x, int t) {
-            if (t >= full_lo && t + ATT_TILE <= full_hi)
-                attend<D, RT, false>(st, x, t, len, lo, hi, g);
-            else
-                attend<D, RT, true>(st, x, t, len, lo, hi, g);
+        const uint8_t *mine = lds + wave * ATT_STAGES * St::BYTES;
+        const uint32_t mine32 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)mine;
+        RowWindow win = row_window(a, table, kvh, t0, STEP, t_last, lane);
+#pragma unroll
+        for (int i = 0; i < ATT_STAGES - 1; i++)
+            copy_tile<D>(a, window_rows(win, i), mine32 + i * St::BYTES, lane);
+        int buf = 0, ahead = ATT_STAGES - 1;         // place in the window of the next copy
+        auto step = [&](auto masked) {
+            if (ahead == 64) {
+                const int tn = t0 + (ATT_STAGES - 1) * STEP;
+                win = row_window(a, table, kvh, tn < t_last ? tn : t_last, STEP, t_last, lane);
+                ahead = 0;
+            }
+            const int fill = buf == 0 ? ATT_STAGES - 1 : buf - 1;
+            copy_tile<D>(a, window_rows(win, ahead), mine32 + fill * St::BYTES, lane);
+            ahead++;
+            wait_copies<(ATT_STAGES - 1) * St::COPIES>();
+            attend<D, RT, decltype(masked)::value>(st, mine32 + buf * St::BYTES, t0, len, lo, hi,
+                                                   l, g);
+            // The tile has been read before the next step's copies overwrite it.
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+            buf = buf == ATT_STAGES - 1 ? 0 : buf + 1;
+            t0 += STEP;
         };
-        KvTile<D> x0, x1;
-        load_tile<D>(x0, a, at(t0), kvh, l, g);
-        TilePages next = at(t0 + STEP);
-        for (;;) {
-            load_tile<D>(x1, a, next, kvh, l, g);
-            next = at(t0 + 2 * STEP);
-            work(x0, t0);
-            if (t0 == t_last)
-                break;
-            load_tile<D>(x0, a, next, kvh, l, g);
-            next = at(t0 + 3 * STEP);
-            work(x1, t0 + STEP);
-            t0 += 2 * STEP;
-            if (t0 > t_last)
-                break;
+        // Loops of their own for tiles that need no mask and for the others: both
+        // forms in one loop took 90 registers more.
+        auto full = [&] { return t0 >= full_lo && t0 + ATT_TILE <= full_hi; };
+        while (t0 <= t_last) {
+            while (t0 <= t_last && full())
+                step(std::false_type{});
+            while (t0 <= t_last && !full())
+                step(std::true_type{});
         }
+        wait_copies<0>();
     }
 
     // Join the four wavefronts.
@@ -571,7 +708,7 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
             lds_ml[wave][16 * rt + l][1] = st.l[rt];
         }
     }
-    __syncthreads();
+    __syncthreads();                                 // no wavefront reads tiles any more
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
         const int r = 16 * rt + l;
@@ -579,7 +716,7 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
 #pragma unroll
         for (int w = 0; w < ATT_WAVES; w++)
             m = __builtin_fmaxf(m, lds_ml[w][r][0]);
-        const float f = __builtin_ldexpf(__builtin_amdgcn_exp2f(st.m[rt] - m), st.e[rt] - 14);
+        const float f = __builtin_amdgcn_exp2f(st.m[rt] - m);
         // Element 4g + i of lane column l, tile j: d = (4g + i) D/16 + j.
 #pragma unroll
         for (int i = 0; i < 4; i++)
@@ -616,7 +753,7 @@ __global__ void __launch_bounds__(ATT_THREADS, RT == 1 && D <= 128 ? 2 : 1)
                        (uint32_t)bf16_rne(o[2 * j + 1] * inv) << 16;
             *reinterpret_cast<u32x4_t *>(a.out + qrow * D + d) = v;
             if (a.lse && d == 0)
-                a.lse[qrow] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * LN2
+                a.lse[qrow] = sum > 0.0f ? (m - TOP + __builtin_amdgcn_logf(sum)) * LN2
                                          : -__builtin_inff();
         } else {
             const int64_t pr = (int64_t)wg_id() * ROWS + r;
@@ -704,7 +841,7 @@ __global__ void __launch_bounds__(256) nvfp4_attention_join_kernel(AttnK a)
     for (int j = 0; j < V; j++)
         a.out[row * D + 64 * j + lane] = bf16_rne(o[j] * inv);
     if (a.lse && lane == 0)
-        a.lse[row] = sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * LN2 : -__builtin_inff();
+        a.lse[row] = sum > 0.0f ? (m - TOP + __builtin_amdgcn_logf(sum)) * LN2 : -__builtin_inff();
 }
 
 // Row tiles of a launch, and the most units its plan can have: a chunk more
@@ -718,11 +855,10 @@ AttnPlan attention_plan(int64_t n_seqs, int64_t q_len, int64_t n_heads, int64_t 
                         int64_t head_dim, int64_t max_keys)
 {
     const int64_t rows = q_len * (n_heads / n_kv_heads);
-    // More rows share a key's decoding, as far as a wavefront's registers go: 64 rows
-    // of 64 elements, 32 of 128, 16 of 256.
-    const int most_rt = head_dim == 64 ? 4 : head_dim == 128 ? 2 : 1;
-    const int want_rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    const int rt = want_rt < most_rt ? want_rt : most_rt;
+    // More rows share a key's decoding, as far as a wavefront's registers go without
+    // spilling: 32 rows of 64 or 128 elements, 16 of 256.  (64 rows of 64 elements:
+    // 202 us against 176 us on chunks of 509 queries over 8192 keys.)
+    const int rt = rows <= 16 || head_dim == 256 ? 1 : 2;
     const int64_t row_tiles = (rows + 16 * rt - 1) / (16 * rt);
     const int64_t base = n_seqs * n_kv_heads * row_tiles;
     // With enough row tiles to fill the chip, or keys for one chunk, none is split.
@@ -766,8 +902,7 @@ hipError_t launch_nvfp4_attention(const AttnArgs &a, void *workspace, hipStream_
     const int64_t wgs = p.units;
     if (a.head_dim == 64)
         p.rt == 1 ? attention_launch<64, 1>(k, wgs, stream)
-        : p.rt == 2 ? attention_launch<64, 2>(k, wgs, stream)
-                    : attention_launch<64, 4>(k, wgs, stream);
+                  : attention_launch<64, 2>(k, wgs, stream);
     else if (a.head_dim == 128)
         p.rt == 1 ? attention_launch<128, 1>(k, wgs, stream)
                   : attention_launch<128, 2>(k, wgs, stream);
