@@ -689,7 +689,7 @@ int mxq_moe_combine_backward(int dtype, const void *d_out, const void *rows, int
  * sx[m] = 1 for BF16 and fp32 activations, x_scales[m] for NVFP4 ones (whose
  * x[m][k] is dec(code) dec(block scale)).  Weights and NVFP4 activations enter
  * the products exactly.  BF16 and fp32 activations are held in FP16 under a
- * power-of-two scale per row and 256 values: BF16 values within 2^-30 of the
+ * power-of-two scale per row and 128 values: BF16 values within 2^-30 of the
  * group's largest magnitude are exact, smaller ones off by at most 2^-39 of it;
  * fp32 values are off by at most 2^-11 relative (or 2^-39 of the largest).
  * Sums are accumulated in fp32.

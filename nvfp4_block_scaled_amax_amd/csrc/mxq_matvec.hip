@@ -2,6 +2,33 @@
 // projections (dense) and experts (expert-sorted rows, the gate/up pair with
 // SwiGLU in the epilogue).  C[m][n] = s_x[m] s_b[n] sum_k x[m][k]
 // dec(code[n][k]) dec(block scale[n][k/16]), fp32 accumulation.
+//
+// What bounds it: the weights, 9/16 byte an element, each read once; the
+// arithmetic is one conversion and one packed multiply per code pair, about
+// half of what the VALU can do while HBM delivers the pair.  So every row
+// count takes the same path: 16x16x32 FP16 matrix instructions with 16 weight
+// rows as their first operand and up to 16 activation rows as the second
+// (rows past M repeat the last one and are not stored).
+//
+// Weights.  dec(code) dec(block scale) is an exact FP16 value.  In a unit of
+// 128 K values lane (n, g) = (lane % 16, lane / 16) holds the 32 values k =
+// 32 g .. of row n: one 16-byte load of codes and two block scales.  Which
+// 8 of them enter instruction q of four is the same for both operands, so
+// the lane's own order serves.
+//
+// Activations are staged once per workgroup in LDS as FP16, 128 values of a
+// row under one power of two (their largest magnitude in [2^14, 2^15)), so
+// that BF16 values enter exactly unless they are 2^-30 below that; per-token
+// NVFP4 ones enter as dec(code) dec(block scale).  A unit's product starts
+// from zero and joins the row's sum under the running largest exponent, so
+// no sum overflows or underflows where the result does not.
+//
+// Split.  The four wavefronts of a workgroup share K (unit by unit) and join
+// through LDS for every 16-row tile of weights: small weights fill more of
+// the chip, and a wavefront has all its loads of a tile in flight.  The next
+// tile's loads are issued before the current tile is computed.
+#include <type_traits>
+
 #include "mxq_layer.h"
 #include "mxq_layer_device.h"
 
@@ -9,140 +36,465 @@ namespace mxq {
 
 namespace {
 
-constexpr int MV_WAVES = 4;
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-// The 16 values of block b of activation row r (NVFP4: without its FP32
-// scale).
-template <int FMT>
-__device__ __forceinline__ void act_block(float (&v)[16], const ActX &x, int64_t r, int64_t b,
-                                          int64_t K)
+constexpr int MV_WAVES = 4, MV_THREADS = 64 * MV_WAVES;
+constexpr int MV_UNIT = 128;                      // K values per unit
+constexpr int MV_XROW = MV_UNIT * 2 + 16;         // a row's unit in LDS, padded: 16 rows at one
+                                                  // offset fall in distinct banks
+constexpr int MV_BLOCK = 4;                       // units a wavefront loads at once
+constexpr int MV_RROW = 20;                       // floats per row of a wavefront's partial tile
+constexpr int MV_MAX_ROWS = 32;                   // activation rows of a workgroup
+constexpr int MV_LDS = 160 * 1024;                // a workgroup's most
+constexpr int64_t MV_TARGET_WGS = 1024;
+
+struct MvArgs {
+    ActX x;
+    WeightB w, up;                                // up.codes == nullptr: no gate
+    const float *scales;
+    int64_t rows_per_scale;
+    int64_t N, K;
+    int rows;                                     // activation rows per pass (dense)
+    int M, passes;                                // dense
+    int tiles, wgs_n;                             // 16-row weight tiles, workgroups sharing them
+    // Experts: rows of x, sorted by segment.
+    int64_t n_tokens, total_rows;
+    const int64_t *row_tokens, *seg_offsets;
+    int n_groups;
+    int chunk_rows;                               // activation rows staged at once
+    void *c;
+};
+
+__device__ __forceinline__ f16x2_t e4m3_pair(uint32_t bytes)
 {
-    if constexpr (FMT == MXQ_X_BF16) {
-        const uint16_t *p = reinterpret_cast<const uint16_t *>(x.x) + r * K + 16 * b;
+    return __builtin_bit_cast(f16x2_t,
+                              __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(bytes, 1.0f, false));
+}
+template <int J>
+__device__ __forceinline__ f16x2_t code_pair(uint32_t codes)
+{
+    return __builtin_bit_cast(f16x2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, J));
+}
+// Eight values (one dword of codes) under block scale d.
+__device__ __forceinline__ f16x8_t oct(uint32_t codes, _Float16 d)
+{
+    const f16x2_t d2 = {d, d};
+    const f16x2_t a = code_pair<0>(codes) * d2, b = code_pair<1>(codes) * d2,
+                  c = code_pair<2>(codes) * d2, e = code_pair<3>(codes) * d2;
+    return f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
+}
+
+// Stages rows [0, rows) of the activations (row r is row src(r) of x) into
+// LDS: 16 lanes a (row, unit), 8 values a lane; columns past K are zero.
+// ex[unit * rows + r] is the unit's exponent.
+template <int FMT, typename Src>
+__device__ __forceinline__ void stage_rows(uint8_t *xs, int *ex, const ActX &x, int rows,
+                                           int units, int64_t K, Src src)
+{
+    const int l16 = (int)(tid() & 15);
+    for (int p = (int)(tid() >> 4); p < rows * units; p += MV_THREADS / 16) {
+        const int u = p / rows, r = p - u * rows;
+        const int64_t row = src(r), k = (int64_t)MV_UNIT * u + 8 * l16;
+        const bool in = k < K;                    // K % 64 == 0: all 8 values or none
+        f16x8_t v = {};
+        int e = 0;
+        if constexpr (FMT == MXQ_X_NVFP4) {
+            if (in) {
+                const uint8_t *c = reinterpret_cast<const uint8_t *>(x.x) + row * (K >> 1) + (k >> 1);
+                v = oct(*reinterpret_cast<const uint32_t *>(c),
+                        e4m3_pair(x.bs[row * (K >> 4) + (k >> 4)])[0]);
+            }
+        } else {
+            float f[8] = {};
+            if (in) {
+                if constexpr (FMT == MXQ_X_BF16) {
+                    const uint4 q = ld16(reinterpret_cast<const uint16_t *>(x.x) + row * K + k);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 16; i++)
-            v[i] = u2f((uint32_t)p[i] << 16);
-    } else if constexpr (FMT == MXQ_X_F32) {
-        const float *p = reinterpret_cast<const float *>(x.x) + r * K + 16 * b;
+                    for (int i = 0; i < 4; i++) {
+                        f[2 * i] = bf16_lo(w[i]);
+                        f[2 * i + 1] = bf16_hi(w[i]);
+                    }
+                } else {
+                    const float *s = reinterpret_cast<const float *>(x.x) + row * K + k;
 #pragma unroll
-        for (int i = 0; i < 16; i++)
-            v[i] = p[i];
-    } else {
-        const uint2 c = ld8(reinterpret_cast<const uint8_t *>(x.x) + r * (K >> 1) + 8 * b);
-        const float d = e4m3_value(x.bs[r * (K >> 4) + b]);
+                    for (int h = 0; h < 2; h++) {
+                        const uint4 q = ld16(s + 4 * h);
+                        f[4 * h] = u2f(q.x);
+                        f[4 * h + 1] = u2f(q.y);
+                        f[4 * h + 2] = u2f(q.z);
+                        f[4 * h + 3] = u2f(q.w);
+                    }
+                }
+            }
+            uint32_t am = 0;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float2_t p = e2m1_values(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu);
-            v[2 * i] = p[0] * d;
-            v[2 * i + 1] = p[1] * d;
+            for (int i = 0; i < 8; i++) {
+                const uint32_t b = f2u(f[i]) & 0x7FFFFFFFu;
+                am = am > b ? am : b;
+            }
+            am = max(am, dpp<DPP_XOR1>(am));
+            am = max(am, dpp<DPP_XOR2>(am));
+            am = max(am, dpp<DPP_HALF_MIRROR>(am));
+            am = max(am, dpp<DPP_MIRROR>(am));
+            e = (int)(am >> 23) - 127 - 14;
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                v[i] = (_Float16)__builtin_ldexpf(f[i], -e);
+        }
+        *reinterpret_cast<f16x8_t *>(xs + (int64_t)p * MV_XROW + 16 * l16) = v;
+        if (l16 == 0)
+            ex[p] = e;
+    }
+}
+
+// One wavefront's loads of up to MV_BLOCK units of a weight tile (of NW
+// weights: gate and up).
+template <int NW>
+struct MvBlock {
+    u32x4_t c[NW][MV_BLOCK];
+    uint32_t s[NW][MV_BLOCK];
+};
+template <int NW>
+__device__ __forceinline__ void load_block(MvBlock<NW> &b, const WeightB *w, int64_t row, int u0,
+                                           int units, int64_t K, int g)
+{
+#pragma unroll
+    for (int j = 0; j < MV_BLOCK; j++) {
+        const int u = u0 + MV_WAVES * j;
+        if (u < units) {
+            // The half unit that ends a K of 64 (mod 128): the upper lane groups read the
+            // lower ones' codes, against zero activations.
+            const int gk = MV_UNIT * u + 32 * g < K ? g : g & 1;
+#pragma unroll
+            for (int i = 0; i < NW; i++) {
+                b.c[i][j] = *reinterpret_cast<const u32x4_t *>(w[i].codes + row * (K >> 1) +
+                                                               64 * u + 16 * gk);
+                b.s[i][j] = *reinterpret_cast<const uint16_t *>(w[i].bs + row * (K >> 4) + 8 * u +
+                                                                2 * gk);
+            }
         }
     }
 }
 
-// Summed in 64 bits: partial sums neither overflow nor underflow where the
-// scaled result does not.
-template <int FMT>
-__device__ __forceinline__ float row_product(const ActX &x, int64_t r, const WeightB &w,
-                                             int64_t n, int64_t K, float scale)
+// A wavefront's sums of one tile: lane (m, g) holds C[m][n0 + 4g + i] of MT
+// groups of 16 activation rows, in units of 2^e.
+template <int NW, int MT>
+struct MvSums {
+    f32x4_t a[NW][MT];
+    int e[MT];
+};
+
+template <int NW, int MT>
+__device__ __forceinline__ void multiply_block(MvSums<NW, MT> &st, const MvBlock<NW> &b,
+                                               const uint8_t *xs, const int *ex, int rows, int u0,
+                                               int units, int l, int g)
 {
-    double sum = 0.0;
-    for (int64_t b = lane_id(); b < K / 16; b += 64) {
-        float v[16];
-        act_block<FMT>(v, x, r, b, K);
-        const uint2 c = ld8(w.codes + n * (K >> 1) + 8 * b);
-        const float d = e4m3_value(w.bs[n * (K >> 4) + b]);
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float2_t p = e2m1_values(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu);
-            sum = __builtin_fma((double)(p[0] * d), (double)v[2 * i], sum);
-            sum = __builtin_fma((double)(p[1] * d), (double)v[2 * i + 1], sum);
+    for (int j = 0; j < MV_BLOCK; j++) {
+        const int u = u0 + MV_WAVES * j;
+        if (u >= units)
+            break;
+        f32x4_t d[NW][MT];
+        int e[MT];
+        const uint8_t *xp[MT];
+#pragma unroll
+        for (int t = 0; t < MT; t++) {
+            const int r = 16 * t + l < rows ? 16 * t + l : rows - 1;
+            xp[t] = xs + (int64_t)(u * rows + r) * MV_XROW + 64 * g;
+            e[t] = ex[u * rows + r];
+#pragma unroll
+            for (int i = 0; i < NW; i++)
+                d[i][t] = f32x4_t{};
+        }
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            f16x8_t xf[MT];
+#pragma unroll
+            for (int t = 0; t < MT; t++)
+                xf[t] = *reinterpret_cast<const f16x8_t *>(xp[t] + 16 * q);
+#pragma unroll
+            for (int i = 0; i < NW; i++) {
+                const f16x8_t wf = oct(b.c[i][j][q], e4m3_pair(b.s[i][j])[q >> 1]);
+#pragma unroll
+                for (int t = 0; t < MT; t++)
+                    d[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, xf[t], d[i][t], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < MT; t++) {
+            const int en = e[t] > st.e[t] ? e[t] : st.e[t];
+            const float fo = __builtin_ldexpf(1.0f, st.e[t] - en), fd = __builtin_ldexpf(1.0f, e[t] - en);
+            st.e[t] = en;
+#pragma unroll
+            for (int i = 0; i < NW; i++)
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    st.a[i][t][k] = __builtin_fmaf(st.a[i][t][k], fo, d[i][t][k] * fd);
         }
     }
-    for (uint32_t m = 1; m < 64; m <<= 1)
-        sum += lane_get(sum, lane_id() ^ m);
-    return (float)(sum * (double)scale);
 }
 
-template <bool BF16_OUT, int FMT>
-__global__ void __launch_bounds__(64 * MV_WAVES) nvfp4_matvec_kernel(
-    ActX x, WeightB b, const float *scales, int64_t rows_per_scale, int64_t M, int64_t N,
-    int64_t K, void *c)
+// The tiles t0, t0 + step, ... of one weight (rows row0 ..) times the staged
+// rows; out(tile, i, m, n) ends each with the sums of weight i.
+template <int NW, int MT, typename Out>
+__device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_t N, int64_t K,
+                                          int tiles, int t0, int step, const uint8_t *xs,
+                                          const int *ex, int rows, int units, float *red,
+                                          int *red_e, MvBlock<NW> &first, Out out)
 {
-    const int64_t n = (int64_t)wg_id() * MV_WAVES + wave_in_group();
-    if (n >= N)
+    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
+    constexpr int PART = 16 * MT * MV_RROW;                  // floats of a wavefront's tile
+    const int blocks = (units + MV_WAVES * MV_BLOCK - 1) / (MV_WAVES * MV_BLOCK);
+    auto tile_row = [&](int t) {
+        const int64_t n = (int64_t)16 * t + l;
+        return row0 + (n < N ? n : N - 1);
+    };
+    MvBlock<NW> cur = first;
+    int parity = 0;
+    for (int t = t0; t < tiles; t += step) {
+        MvSums<NW, MT> st;
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+            st.e[i] = -300;
+#pragma unroll
+            for (int k = 0; k < NW; k++)
+                st.a[k][i] = f32x4_t{};
+        }
+        for (int b = 0; b < blocks; b++) {
+            MvBlock<NW> nx;
+            const bool more = b + 1 < blocks;
+            if (more || t + step < tiles)
+                load_block<NW>(nx, w, tile_row(more ? t : t + step),
+                               wave + (more ? MV_WAVES * MV_BLOCK * (b + 1) : 0), units, K, g);
+            multiply_block<NW, MT>(st, cur, xs, ex, rows, wave + MV_WAVES * MV_BLOCK * b, units,
+                                   l, g);
+            cur = nx;
+        }
+        float *mine = red + (parity * MV_WAVES + wave) * NW * PART;
+        int *mine_e = red_e + (parity * MV_WAVES + wave) * 16 * MT;
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+            if (g == 0)
+                mine_e[16 * i + l] = st.e[i];
+#pragma unroll
+            for (int k = 0; k < NW; k++)
+                *reinterpret_cast<f32x4_t *>(mine + k * PART + (16 * i + l) * MV_RROW + 4 * g) =
+                    st.a[k][i];
+        }
+        __syncthreads();
+        // Tile t's partials are read here and overwritten two tiles on, behind the next
+        // tile's barrier.
+        for (int o = (int)tid(); o < 16 * rows; o += MV_THREADS) {
+            const int m = o >> 4, n = o & 15;
+            int e = -300;
+#pragma unroll
+            for (int v = 0; v < MV_WAVES; v++) {
+                const int ev = red_e[(parity * MV_WAVES + v) * 16 * MT + m];
+                e = e > ev ? e : ev;
+            }
+            float s[NW];
+#pragma unroll
+            for (int k = 0; k < NW; k++) {
+                s[k] = 0.0f;
+#pragma unroll
+                for (int v = 0; v < MV_WAVES; v++)
+                    s[k] += __builtin_ldexpf(red[(parity * MV_WAVES + v) * NW * PART + k * PART +
+                                                 m * MV_RROW + n],
+                                             red_e[(parity * MV_WAVES + v) * 16 * MT + m] - e);
+            }
+            if ((int64_t)16 * t + n < N)
+                out(m, (int64_t)16 * t + n, s, e);
+        }
+        parity ^= 1;
+    }
+}
+
+// LDS of a launch: staged rows, their exponents, two parities of partials.
+struct MvLds {
+    int ex, red, red_e, bytes;
+};
+__host__ __device__ inline MvLds mv_lds(int rows, int units, int nw, int mt)
+{
+    MvLds o;
+    o.ex = rows * units * MV_XROW;
+    o.red = o.ex + (rows * units * 4 + 15) / 16 * 16;
+    o.red_e = o.red + 2 * MV_WAVES * nw * 16 * mt * MV_RROW * 4;
+    o.bytes = o.red_e + 2 * MV_WAVES * 16 * mt * 4;
+    return o;
+}
+
+template <bool BF16_OUT, int FMT, int MT>
+__global__ void __launch_bounds__(MV_THREADS) nvfp4_matvec_kernel(MvArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int units = (int)((a.K + MV_UNIT - 1) / MV_UNIT);
+    const int t0 = (int)(wg_id() / (uint32_t)a.passes), pass = (int)(wg_id() % (uint32_t)a.passes);
+    const int m0 = pass * a.rows, rows = a.M - m0 < a.rows ? a.M - m0 : a.rows;
+    const MvLds o = mv_lds(a.rows, units, 1, MT);
+    int *ex = reinterpret_cast<int *>(lds + o.ex);
+    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4;
+    MvBlock<1> first;
+    const int64_t n = (int64_t)16 * t0 + l;
+    load_block<1>(first, &a.w, n < a.N ? n : a.N - 1, wave_in_group(), units, a.K, g);
+    stage_rows<FMT>(lds, ex, a.x, rows, units, a.K, [&](int r) { return (int64_t)m0 + r; });
+    __syncthreads();
+    run_tiles<1, MT>(&a.w, 0, a.N, a.K, a.tiles, t0, a.wgs_n, lds, ex, rows, units,
+                     reinterpret_cast<float *>(lds + o.red), reinterpret_cast<int *>(lds + o.red_e),
+                     first, [&](int m, int64_t nn, const float *s, int e) {
+                         float v = s[0] * a.scales[nn / a.rows_per_scale];
+                         if constexpr (FMT == MXQ_X_NVFP4)
+                             v *= a.x.s[m0 + m];
+                         st_elem<BF16_OUT>(a.c, (m0 + m) * a.N + nn, __builtin_ldexpf(v, e));
+                     });
+}
+
+// The expert of slot s (the s-th segment that has rows) and its rows.
+__device__ __forceinline__ bool find_segment(const int64_t *off, int n_groups, int64_t total,
+                                             int slot, int *expert, int64_t *r0, int64_t *r1)
+{
+    const int lane = (int)lane_id();
+    for (int e0 = 0; e0 < n_groups; e0 += 64) {
+        const int e = e0 + lane;
+        int64_t a = 0, b = 0;
+        if (e < n_groups) {
+            a = off[e];
+            b = off[e + 1];
+            a = a < 0 ? 0 : a;
+            b = b > total ? total : b;
+        }
+        uint64_t some = __builtin_amdgcn_ballot_w64(b > a);
+        const int n = __builtin_popcountll(some);
+        if (slot < n) {
+            for (; slot > 0; slot--)
+                some &= some - 1;
+            const int src = __builtin_ctzll(some);
+            *expert = e0 + src;
+            *r0 = __builtin_amdgcn_readlane((int)a, src);    // at most 2^30 rows
+            *r1 = __builtin_amdgcn_readlane((int)b, src);
+            return true;
+        }
+        slot -= n;
+    }
+    return false;
+}
+
+template <bool BF16_OUT, int FMT, int MT, bool GATED>
+__global__ void __launch_bounds__(MV_THREADS) nvfp4_expert_kernel(MvArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int NW = GATED ? 2 : 1;
+    const int units = (int)((a.K + MV_UNIT - 1) / MV_UNIT);
+    const int t0 = (int)(wg_id() % (uint32_t)a.wgs_n);
+    int e = 0;
+    int64_t r0 = 0, r1 = 0;
+    if (!find_segment(a.seg_offsets, a.n_groups, a.total_rows, (int)(wg_id() / (uint32_t)a.wgs_n),
+                      &e, &r0, &r1))
         return;
-    const float sb = scales[n / rows_per_scale];
-    for (int64_t m = 0; m < M; m++) {
-        const float s = row_product<FMT>(x, m, b, n, K, FMT == MXQ_X_NVFP4 ? sb * x.s[m] : sb);
-        if (lane_id() == 0)
-            st_elem<BF16_OUT>(c, m * N + n, s);
+    const MvLds o = mv_lds(a.chunk_rows, units, NW, MT);
+    int *ex = reinterpret_cast<int *>(lds + o.ex);
+    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4;
+    const WeightB w[2] = {a.w, a.up};
+    const int64_t row0 = (int64_t)e * a.N, n = (int64_t)16 * t0 + l;
+    const float scale = a.scales[e];
+    for (int64_t c0 = r0; c0 < r1; c0 += a.chunk_rows) {
+        const int rows = (int)(r1 - c0 < a.chunk_rows ? r1 - c0 : a.chunk_rows);
+        auto src = [&](int r) {
+            int64_t x = c0 + r;
+            if constexpr (GATED) {
+                x = a.row_tokens[x];
+                x = x < 0 ? 0 : x >= a.n_tokens ? a.n_tokens - 1 : x;
+            }
+            return x;
+        };
+        MvBlock<NW> first;
+        load_block<NW>(first, w, row0 + (n < a.N ? n : a.N - 1), wave_in_group(), units, a.K, g);
+        if (c0 != r0)
+            __syncthreads();                      // the last chunk's rows have been read
+        stage_rows<FMT>(lds, ex, a.x, rows, units, a.K, src);
+        __syncthreads();
+        run_tiles<NW, MT>(w, row0, a.N, a.K, a.tiles, t0, a.wgs_n, lds, ex, rows, units,
+                          reinterpret_cast<float *>(lds + o.red),
+                          reinterpret_cast<int *>(lds + o.red_e), first,
+                          [&](int m, int64_t nn, const float *s, int ee) {
+                              float sx = 1.0f;
+                              if constexpr (FMT == MXQ_X_NVFP4)
+                                  sx = a.x.s[src(m)];
+                              float v = __builtin_ldexpf(s[0] * scale * sx, ee);
+                              if constexpr (GATED)
+                                  v = silu_f32(v) * __builtin_ldexpf(s[NW - 1] * scale * sx, ee);
+                              st_elem<BF16_OUT>(a.c, (c0 + m) * a.N + nn, v);
+                          });
     }
 }
 
-template <bool BF16_OUT, int FMT>
-__global__ void __launch_bounds__(64 * MV_WAVES) nvfp4_expert_kernel(
-    ActX x, int64_t n_tokens, const int64_t *row_tokens, const int64_t *seg_offsets,
-    int64_t n_tiles, int64_t total_rows, WeightB w, WeightB up, const float *scales, int64_t N,
-    int64_t K, void *c)
+// Rows staged at once: at most `want`, as LDS holds them beside the partial
+// tiles of nw weights (one row of the largest K always fits).
+int staged_rows(int64_t want, int64_t K, int nw)
 {
-    const int64_t e = wg_id() / (uint32_t)n_tiles, tile = wg_id() % (uint32_t)n_tiles;
-    const int64_t n = tile * MV_WAVES + wave_in_group();
-    if (n >= N)
-        return;
-    int64_t r0 = seg_offsets[e], r1 = seg_offsets[e + 1];
-    r0 = r0 < 0 ? 0 : r0;
-    r1 = r1 > total_rows ? total_rows : r1;
-    for (int64_t r = r0; r < r1; r++) {
-        int64_t xr = r;
-        if (row_tokens) {
-            xr = row_tokens[r];
-            xr = xr < 0 ? 0 : xr >= n_tokens ? n_tokens - 1 : xr;
-        }
-        const float s = (FMT == MXQ_X_NVFP4 ? x.s[xr] : 1.0f) * scales[e];
-        float g = row_product<FMT>(x, xr, w, e * N + n, K, s);
-        if (up.codes) {
-            const float u = row_product<FMT>(x, xr, up, e * N + n, K, s);
-            g = silu_f32(g) * u;
-        }
-        if (lane_id() == 0)
-            st_elem<BF16_OUT>(c, r * N + n, g);
-    }
+    const int units = (int)((K + MV_UNIT - 1) / MV_UNIT);
+    int r = (int)(want < MV_MAX_ROWS ? want : MV_MAX_ROWS);
+    while (r > 1 && mv_lds(r, units, nw, (r + 15) / 16).bytes > MV_LDS)
+        r--;
+    return r;
+}
+
+template <typename F>
+void with_format(int fmt, bool bf16_out, F f)
+{
+    auto by_out = [&](auto format) {
+        if (bf16_out)
+            f(std::true_type{}, format);
+        else
+            f(std::false_type{}, format);
+    };
+    if (fmt == MXQ_X_BF16)
+        by_out(std::integral_constant<int, MXQ_X_BF16>{});
+    else if (fmt == MXQ_X_F32)
+        by_out(std::integral_constant<int, MXQ_X_F32>{});
+    else
+        by_out(std::integral_constant<int, MXQ_X_NVFP4>{});
 }
 
 }  // namespace
-
-#define MV_DISPATCH(KERNEL, ...)                                                                  \
-    do {                                                                                          \
-        if (bf16_out) {                                                                           \
-            if (x.fmt == MXQ_X_BF16)                                                              \
-                hipLaunchKernelGGL((KERNEL<true, MXQ_X_BF16>), __VA_ARGS__);                      \
-            else if (x.fmt == MXQ_X_F32)                                                          \
-                hipLaunchKernelGGL((KERNEL<true, MXQ_X_F32>), __VA_ARGS__);                       \
-            else                                                                                  \
-                hipLaunchKernelGGL((KERNEL<true, MXQ_X_NVFP4>), __VA_ARGS__);                     \
-        } else {                                                                                  \
-            if (x.fmt == MXQ_X_BF16)                                                              \
-                hipLaunchKernelGGL((KERNEL<false, MXQ_X_BF16>), __VA_ARGS__);                     \
-            else if (x.fmt == MXQ_X_F32)                                                          \
-                hipLaunchKernelGGL((KERNEL<false, MXQ_X_F32>), __VA_ARGS__);                      \
-            else                                                                                  \
-                hipLaunchKernelGGL((KERNEL<false, MXQ_X_NVFP4>), __VA_ARGS__);                    \
-        }                                                                                         \
-    } while (0)
 
 hipError_t launch_nvfp4_matvec(const ActX &x, const WeightB &b, const float *scales,
                                int64_t rows_per_scale, int64_t M, int64_t N, int64_t K,
                                bool bf16_out, void *c, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((N + MV_WAVES - 1) / MV_WAVES)), block(64 * MV_WAVES);
-    MV_DISPATCH(nvfp4_matvec_kernel, grid, block, 0, stream, x, b, scales, rows_per_scale, M, N,
-                K, c);
+    MvArgs a{};
+    a.x = x;
+    a.w = b;
+    a.scales = scales;
+    a.rows_per_scale = rows_per_scale;
+    a.N = N;
+    a.K = K;
+    a.M = (int)M;
+    const int most = staged_rows(M, K, 1);
+    a.passes = (int)((M + most - 1) / most);
+    a.rows = (int)((M + a.passes - 1) / a.passes);
+    a.tiles = (int)((N + 15) / 16);
+    const int64_t share = MV_TARGET_WGS / a.passes < 1 ? 1 : MV_TARGET_WGS / a.passes;
+    a.wgs_n = (int)(a.tiles < share ? a.tiles : share);
+    a.c = c;
+    const int mt = (a.rows + 15) / 16, units = (int)((K + MV_UNIT - 1) / MV_UNIT);
+    const size_t lds = (size_t)mv_lds(a.rows, units, 1, mt).bytes;
+    const dim3 grid((unsigned)(a.wgs_n * a.passes)), block(MV_THREADS);
+    with_format(x.fmt, bf16_out, [&](auto out, auto fmt) {
+        constexpr bool OUT = decltype(out)::value;
+        constexpr int FMT = decltype(fmt)::value;
+        if (mt == 1)
+            hipLaunchKernelGGL((nvfp4_matvec_kernel<OUT, FMT, 1>), grid, block, lds, stream, a);
+        else
+            hipLaunchKernelGGL((nvfp4_matvec_kernel<OUT, FMT, 2>), grid, block, lds, stream, a);
+    });
     return hipGetLastError();
 }
 
 bool expert_grid_ok(int64_t n_groups, int64_t, int64_t N)
 {
-    return n_groups * ((N + MV_WAVES - 1) / MV_WAVES) < ((int64_t)1 << 24);
+    return n_groups * ((N + 3) / 4) < ((int64_t)1 << 24);
 }
 
 hipError_t launch_nvfp4_expert_matvec(const ActX &x, int64_t n_tokens, const int64_t *row_tokens,
@@ -151,10 +503,45 @@ hipError_t launch_nvfp4_expert_matvec(const ActX &x, int64_t n_tokens, const int
                                       const float *scales, int64_t N, int64_t K, bool bf16_out,
                                       void *c, hipStream_t stream)
 {
-    const int64_t n_tiles = (N + MV_WAVES - 1) / MV_WAVES;
-    const dim3 grid((unsigned)(n_tiles * n_groups)), block(64 * MV_WAVES);
-    MV_DISPATCH(nvfp4_expert_kernel, grid, block, 0, stream, x, n_tokens, row_tokens, seg_offsets,
-                n_tiles, total_rows, w, up, scales, N, K, c);
+    MvArgs a{};
+    a.x = x;
+    a.w = w;
+    a.up = up;
+    a.scales = scales;
+    a.N = N;
+    a.K = K;
+    a.n_tokens = n_tokens;
+    a.total_rows = total_rows;
+    a.row_tokens = row_tokens;
+    a.seg_offsets = seg_offsets;
+    a.n_groups = (int)n_groups;
+    a.tiles = (int)((N + 15) / 16);
+    a.c = c;
+    // One slot per expert that can have rows, each shared by enough workgroups that the
+    // launch has about MV_TARGET_WGS.
+    const int64_t slots = n_groups < total_rows ? n_groups : total_rows;
+    int64_t per = (MV_TARGET_WGS + slots - 1) / slots;
+    a.wgs_n = (int)(a.tiles < per ? a.tiles : per);
+    // Rows staged at once: twice an even share of the rows (a fuller expert takes more
+    // chunks), 16 at least.
+    const int64_t even = 2 * ((total_rows + slots - 1) / slots);
+    const bool gated = up.codes != nullptr;
+    a.chunk_rows = staged_rows(total_rows < 16 ? total_rows : even < 16 ? 16 : even, K,
+                               gated ? 2 : 1);
+    const int mt = (a.chunk_rows + 15) / 16, units = (int)((K + MV_UNIT - 1) / MV_UNIT);
+    const size_t lds = (size_t)mv_lds(a.chunk_rows, units, gated ? 2 : 1, mt).bytes;
+    const dim3 grid((unsigned)(a.wgs_n * slots)), block(MV_THREADS);
+    with_format(x.fmt, bf16_out, [&](auto out, auto fmt) {
+        constexpr bool OUT = decltype(out)::value;
+        constexpr int FMT = decltype(fmt)::value;
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, stream, a); };
+        if (mt == 1)
+            gated ? go(nvfp4_expert_kernel<OUT, FMT, 1, true>)
+                  : go(nvfp4_expert_kernel<OUT, FMT, 1, false>);
+        else
+            gated ? go(nvfp4_expert_kernel<OUT, FMT, 2, true>)
+                  : go(nvfp4_expert_kernel<OUT, FMT, 2, false>);
+    });
     return hipGetLastError();
 }
 
