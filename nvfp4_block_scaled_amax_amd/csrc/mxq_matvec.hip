@@ -39,21 +39,35 @@ namespace {
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int MV_WAVES = 4, MV_THREADS = 64 * MV_WAVES;
+#ifndef MVP
+#define MVP 16
+#define MVW 8
+#define MVK 2048
+#define MVB1 4
+#define MVB2 2
+#endif
+// Wavefronts of a workgroup that splits K among them, and of one whose wavefronts
+// take whole tiles: there more of them share the staged rows (13 x 128257 x 2048:
+// 47 us with four, two workgroups a compute unit, YYY us with eight).
+constexpr int mv_waves(int ks) { return ks == 1 ? MVW : 4; }
 constexpr int MV_UNIT = 128;                      // K values per unit
 constexpr int MV_XROW = MV_UNIT * 2 + 16;         // a row's unit in LDS, padded: 16 rows at one
                                                   // offset fall in distinct banks
-constexpr int MV_BLOCK = 4;                       // units a wavefront loads at once
+constexpr int MV_STAGE = 4;                       // units of rows loaded at once when staging
 constexpr int MV_RROW = 20;                       // floats per row of a wavefront's partial tile
 constexpr int MV_MAX_ROWS = 32;                   // activation rows of a workgroup
 constexpr int MV_LDS = 160 * 1024;                // a workgroup's most
-constexpr int64_t MV_TARGET_WGS = 1024;
+constexpr int64_t MV_CU_WAVES = MVP;
+constexpr int64_t MV_WHOLE_K_TILES = MVK;
+
+// Units a wavefront loads at once of nw weights.
+constexpr int mv_block(int nw) { return nw == 1 ? MVB1 : MVB2; }
 
 struct MvArgs {
     ActX x;
     WeightB w, up;                                // up.codes == nullptr: no gate
     const float *scales;
-    int64_t rows_per_scale;
+    Div per_scale;                                // rows of the weight per FP32 scale
     int64_t N, K;
     int rows;                                     // activation rows per pass (dense)
     int M, passes;                                // dense
@@ -85,84 +99,106 @@ __device__ __forceinline__ f16x8_t oct(uint32_t codes, _Float16 d)
     return f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
 }
 
-// Stages rows [0, rows) of the activations (row r is row src(r) of x) into
-// LDS: 16 lanes a (row, unit), 8 values a lane; columns past K are zero.
-// ex[unit * rows + r] is the unit's exponent.
-template <int FMT, typename Src>
-__device__ __forceinline__ void stage_rows(uint8_t *xs, int *ex, const ActX &x, int rows,
-                                           int units, int64_t K, Src src)
+// What a lane loads of an activation row's unit: 8 values.
+struct ActRaw {
+    uint4 a, b;
+};
+template <int FMT>
+__device__ __forceinline__ ActRaw act_load(const ActX &x, int64_t row, int64_t k, int64_t K)
 {
-    const int l16 = (int)(tid() & 15);
-    for (int p = (int)(tid() >> 4); p < rows * units; p += MV_THREADS / 16) {
-        const int u = p / rows, r = p - u * rows;
-        const int64_t row = src(r), k = (int64_t)MV_UNIT * u + 8 * l16;
-        const bool in = k < K;                    // K % 64 == 0: all 8 values or none
-        f16x8_t v = {};
-        int e = 0;
-        if constexpr (FMT == MXQ_X_NVFP4) {
-            if (in) {
-                const uint8_t *c = reinterpret_cast<const uint8_t *>(x.x) + row * (K >> 1) + (k >> 1);
-                v = oct(*reinterpret_cast<const uint32_t *>(c),
-                        e4m3_pair(x.bs[row * (K >> 4) + (k >> 4)])[0]);
-            }
-        } else {
-            float f[8] = {};
-            if (in) {
-                if constexpr (FMT == MXQ_X_BF16) {
-                    const uint4 q = ld16(reinterpret_cast<const uint16_t *>(x.x) + row * K + k);
-                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    ActRaw r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (k >= K)                                   // K % 64 == 0: all 8 values or none
+        return r;
+    if constexpr (FMT == MXQ_X_BF16) {
+        r.a = ld16(reinterpret_cast<const uint16_t *>(x.x) + row * K + k);
+    } else if constexpr (FMT == MXQ_X_F32) {
+        r.a = ld16(reinterpret_cast<const float *>(x.x) + row * K + k);
+        r.b = ld16(reinterpret_cast<const float *>(x.x) + row * K + k + 4);
+    } else {
+        r.a.x = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(x.x) +
+                                                    row * (K >> 1) + (k >> 1));
+        r.a.y = x.bs[row * (K >> 4) + (k >> 4)];
+    }
+    return r;
+}
+// The FP16 values of a row's unit (16 lanes, 8 values each) and its exponent.
+template <int FMT>
+__device__ __forceinline__ f16x8_t act_f16(const ActRaw &r, int *e)
+{
+    if constexpr (FMT == MXQ_X_NVFP4) {
+        *e = 0;
+        return oct(r.a.x, e4m3_pair(r.a.y)[0]);
+    } else {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+        float f[8];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        f[2 * i] = bf16_lo(w[i]);
-                        f[2 * i + 1] = bf16_hi(w[i]);
-                    }
-                } else {
-                    const float *s = reinterpret_cast<const float *>(x.x) + row * K + k;
+        for (int i = 0; i < 8; i++)
+            f[i] = FMT == MXQ_X_F32 ? u2f(w[i]) : (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+        uint32_t am = 0;
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const uint4 q = ld16(s + 4 * h);
-                        f[4 * h] = u2f(q.x);
-                        f[4 * h + 1] = u2f(q.y);
-                        f[4 * h + 2] = u2f(q.z);
-                        f[4 * h + 3] = u2f(q.w);
-                    }
-                }
-            }
-            uint32_t am = 0;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const uint32_t b = f2u(f[i]) & 0x7FFFFFFFu;
-                am = am > b ? am : b;
-            }
-            am = max(am, dpp<DPP_XOR1>(am));
-            am = max(am, dpp<DPP_XOR2>(am));
-            am = max(am, dpp<DPP_HALF_MIRROR>(am));
-            am = max(am, dpp<DPP_MIRROR>(am));
-            e = (int)(am >> 23) - 127 - 14;
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                v[i] = (_Float16)__builtin_ldexpf(f[i], -e);
+        for (int i = 0; i < 8; i++) {
+            const uint32_t b = f2u(f[i]) & 0x7FFFFFFFu;
+            am = am > b ? am : b;
         }
-        *reinterpret_cast<f16x8_t *>(xs + (int64_t)p * MV_XROW + 16 * l16) = v;
-        if (l16 == 0)
-            ex[p] = e;
+        am = max(am, dpp<DPP_XOR1>(am));
+        am = max(am, dpp<DPP_XOR2>(am));
+        am = max(am, dpp<DPP_HALF_MIRROR>(am));
+        am = max(am, dpp<DPP_MIRROR>(am));
+        *e = (int)(am >> 23) - 127 - 14;
+        f16x8_t v;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            v[i] = (_Float16)__builtin_ldexpf(f[i], -*e);
+        return v;
     }
 }
 
-// One wavefront's loads of up to MV_BLOCK units of a weight tile (of NW
+// Stages rows [0, rows) of the activations (row r is row src(r) of x) into
+// LDS; columns past K are zero.  ex[unit * rows + r] is the unit's exponent.
+// Each 16 lanes take a unit of a row, MV_STAGE of them loaded at once.
+template <int FMT, int THREADS, typename Src>
+__device__ __forceinline__ void stage_rows(uint8_t *xs, int *ex, const ActX &x, int rows,
+                                           int units, int64_t K, Src src)
+{
+    constexpr int GROUPS = THREADS / 16;
+    const int l16 = (int)(tid() & 15), total = rows * units;
+    for (int p0 = (int)(tid() >> 4); p0 < total; p0 += GROUPS * MV_STAGE) {
+        ActRaw raw[MV_STAGE];
+#pragma unroll
+        for (int j = 0; j < MV_STAGE; j++) {
+            const int p = p0 + GROUPS * j < total ? p0 + GROUPS * j : total - 1;
+            const int u = (int)((uint32_t)p / (uint32_t)rows);
+            raw[j] = act_load<FMT>(x, src(p - u * rows), (int64_t)MV_UNIT * u + 8 * l16, K);
+        }
+#pragma unroll
+        for (int j = 0; j < MV_STAGE; j++) {
+            const int p = p0 + GROUPS * j;
+            int e;
+            const f16x8_t v = act_f16<FMT>(raw[j], &e);
+            if (p < total) {
+                *reinterpret_cast<f16x8_t *>(xs + p * MV_XROW + 16 * l16) = v;
+                if (l16 == 0)
+                    ex[p] = e;
+            }
+        }
+    }
+}
+
+// One wavefront's loads of up to mv_block units of a weight tile (of NW
 // weights: gate and up).
 template <int NW>
 struct MvBlock {
-    u32x4_t c[NW][MV_BLOCK];
-    uint32_t s[NW][MV_BLOCK];
+    static constexpr int U = mv_block(NW);
+    u32x4_t c[NW][U];
+    uint32_t s[NW][U];
 };
-template <int NW>
+template <int NW, int KS>
 __device__ __forceinline__ void load_block(MvBlock<NW> &b, const WeightB *w, int64_t row, int u0,
                                            int units, int64_t K, int g)
 {
 #pragma unroll
-    for (int j = 0; j < MV_BLOCK; j++) {
-        const int u = u0 + MV_WAVES * j;
+    for (int j = 0; j < mv_block(NW); j++) {
+        const int u = u0 + KS * j;
         if (u < units) {
             // The half unit that ends a K of 64 (mod 128): the upper lane groups read the
             // lower ones' codes, against zero activations.
@@ -186,14 +222,14 @@ struct MvSums {
     int e[MT];
 };
 
-template <int NW, int MT>
+template <int NW, int MT, int KS>
 __device__ __forceinline__ void multiply_block(MvSums<NW, MT> &st, const MvBlock<NW> &b,
                                                const uint8_t *xs, const int *ex, int rows, int u0,
                                                int units, int l, int g)
 {
 #pragma unroll
-    for (int j = 0; j < MV_BLOCK; j++) {
-        const int u = u0 + MV_WAVES * j;
+    for (int j = 0; j < mv_block(NW); j++) {
+        const int u = u0 + KS * j;
         if (u >= units)
             break;
         f32x4_t d[NW][MT];
@@ -236,9 +272,18 @@ __device__ __forceinline__ void multiply_block(MvSums<NW, MT> &st, const MvBlock
     }
 }
 
+// A wavefront's place in the split: KS = 4, the workgroup's wavefronts share K
+// (wavefront w takes units w, w + 4, ...) and each tile is the workgroup's;
+// KS = 1, a tile is one wavefront's and its wavefronts take consecutive ones.
+template <int KS>
+__device__ __forceinline__ int first_tile(int wg) { return KS == 1 ? mv_waves(1) * wg + wave_in_group() : wg; }
+template <int KS>
+__device__ __forceinline__ int first_unit() { return KS == 1 ? 0 : wave_in_group(); }
+
 // The tiles t0, t0 + step, ... of one weight (rows row0 ..) times the staged
-// rows; out(tile, i, m, n) ends each with the sums of weight i.
-template <int NW, int MT, typename Out>
+// rows; out(m, n, sums, e) ends each element with the sums of the NW weights
+// in units of 2^e.
+template <int NW, int MT, int KS, typename Out>
 __device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_t N, int64_t K,
                                           int tiles, int t0, int step, const uint8_t *xs,
                                           const int *ex, int rows, int units, float *red,
@@ -246,7 +291,8 @@ __device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_
 {
     const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
     constexpr int PART = 16 * MT * MV_RROW;                  // floats of a wavefront's tile
-    const int blocks = (units + MV_WAVES * MV_BLOCK - 1) / (MV_WAVES * MV_BLOCK);
+    constexpr int SPAN = KS * mv_block(NW);                      // units of a block
+    const int blocks = (units + SPAN - 1) / SPAN, u0 = first_unit<KS>();
     auto tile_row = [&](int t) {
         const int64_t n = (int64_t)16 * t + l;
         return row0 + (n < N ? n : N - 1);
@@ -266,48 +312,64 @@ __device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_
             MvBlock<NW> nx;
             const bool more = b + 1 < blocks;
             if (more || t + step < tiles)
-                load_block<NW>(nx, w, tile_row(more ? t : t + step),
-                               wave + (more ? MV_WAVES * MV_BLOCK * (b + 1) : 0), units, K, g);
-            multiply_block<NW, MT>(st, cur, xs, ex, rows, wave + MV_WAVES * MV_BLOCK * b, units,
-                                   l, g);
+                load_block<NW, KS>(nx, w, tile_row(more ? t : t + step),
+                                   u0 + (more ? SPAN * (b + 1) : 0), units, K, g);
+            multiply_block<NW, MT, KS>(st, cur, xs, ex, rows, u0 + SPAN * b, units, l, g);
             cur = nx;
         }
-        float *mine = red + (parity * MV_WAVES + wave) * NW * PART;
-        int *mine_e = red_e + (parity * MV_WAVES + wave) * 16 * MT;
+        if constexpr (KS == 1) {
+            // Lane (m, g) holds four consecutive columns of row m.
 #pragma unroll
-        for (int i = 0; i < MT; i++) {
-            if (g == 0)
-                mine_e[16 * i + l] = st.e[i];
+            for (int i = 0; i < MT; i++)
+                if (16 * i + l < rows)
 #pragma unroll
-            for (int k = 0; k < NW; k++)
-                *reinterpret_cast<f32x4_t *>(mine + k * PART + (16 * i + l) * MV_RROW + 4 * g) =
-                    st.a[k][i];
-        }
-        __syncthreads();
-        // Tile t's partials are read here and overwritten two tiles on, behind the next
-        // tile's barrier.
-        for (int o = (int)tid(); o < 16 * rows; o += MV_THREADS) {
-            const int m = o >> 4, n = o & 15;
-            int e = -300;
+                    for (int c = 0; c < 4; c++) {
+                        const int64_t n = (int64_t)16 * t + 4 * g + c;
+                        float v[NW];
 #pragma unroll
-            for (int v = 0; v < MV_WAVES; v++) {
-                const int ev = red_e[(parity * MV_WAVES + v) * 16 * MT + m];
-                e = e > ev ? e : ev;
+                        for (int k = 0; k < NW; k++)
+                            v[k] = st.a[k][i][c];
+                        if (n < N)
+                            out(16 * i + l, n, v, st.e[i]);
+                    }
+        } else {
+            float *mine = red + (parity * KS + wave) * NW * PART;
+            int *mine_e = red_e + (parity * KS + wave) * 16 * MT;
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+                if (g == 0)
+                    mine_e[16 * i + l] = st.e[i];
+#pragma unroll
+                for (int k = 0; k < NW; k++)
+                    *reinterpret_cast<f32x4_t *>(mine + k * PART + (16 * i + l) * MV_RROW +
+                                                 4 * g) = st.a[k][i];
             }
-            float s[NW];
+            __syncthreads();
+            // Tile t's partials are read here and overwritten two tiles on, behind the
+            // next tile's barrier.
+            for (int o = (int)tid(); o < 16 * rows; o += 64 * KS) {
+                const int m = o >> 4, n = o & 15;
+                int e = -300;
 #pragma unroll
-            for (int k = 0; k < NW; k++) {
-                s[k] = 0.0f;
+                for (int v = 0; v < KS; v++) {
+                    const int ev = red_e[(parity * KS + v) * 16 * MT + m];
+                    e = e > ev ? e : ev;
+                }
+                float s[NW];
 #pragma unroll
-                for (int v = 0; v < MV_WAVES; v++)
-                    s[k] += __builtin_ldexpf(red[(parity * MV_WAVES + v) * NW * PART + k * PART +
-                                                 m * MV_RROW + n],
-                                             red_e[(parity * MV_WAVES + v) * 16 * MT + m] - e);
+                for (int k = 0; k < NW; k++) {
+                    s[k] = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < KS; v++)
+                        s[k] += __builtin_ldexpf(
+                            red[(parity * KS + v) * NW * PART + k * PART + m * MV_RROW + n],
+                            red_e[(parity * KS + v) * 16 * MT + m] - e);
+                }
+                if ((int64_t)16 * t + n < N)
+                    out(m, (int64_t)16 * t + n, s, e);
             }
-            if ((int64_t)16 * t + n < N)
-                out(m, (int64_t)16 * t + n, s, e);
+            parity ^= 1;
         }
-        parity ^= 1;
     }
 }
 
@@ -315,35 +377,36 @@ __device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_
 struct MvLds {
     int ex, red, red_e, bytes;
 };
-__host__ __device__ inline MvLds mv_lds(int rows, int units, int nw, int mt)
+__host__ __device__ inline MvLds mv_lds(int rows, int units, int nw, int mt, int ks)
 {
     MvLds o;
     o.ex = rows * units * MV_XROW;
     o.red = o.ex + (rows * units * 4 + 15) / 16 * 16;
-    o.red_e = o.red + 2 * MV_WAVES * nw * 16 * mt * MV_RROW * 4;
-    o.bytes = o.red_e + 2 * MV_WAVES * 16 * mt * 4;
+    o.red_e = o.red + (ks == 1 ? 0 : 2 * ks * nw * 16 * mt * MV_RROW * 4);
+    o.bytes = o.red_e + (ks == 1 ? 0 : 2 * ks * 16 * mt * 4);
     return o;
 }
 
-template <bool BF16_OUT, int FMT, int MT>
-__global__ void __launch_bounds__(MV_THREADS) nvfp4_matvec_kernel(MvArgs a)
+template <bool BF16_OUT, int FMT, int MT, int KS>
+__global__ void __launch_bounds__(64 * mv_waves(KS)) nvfp4_matvec_kernel(MvArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int units = (int)((a.K + MV_UNIT - 1) / MV_UNIT);
-    const int t0 = (int)(wg_id() / (uint32_t)a.passes), pass = (int)(wg_id() % (uint32_t)a.passes);
+    const int wg = (int)(wg_id() / (uint32_t)a.passes), t0 = first_tile<KS>(wg);
+    const int pass = (int)(wg_id() % (uint32_t)a.passes);
     const int m0 = pass * a.rows, rows = a.M - m0 < a.rows ? a.M - m0 : a.rows;
-    const MvLds o = mv_lds(a.rows, units, 1, MT);
+    const MvLds o = mv_lds(a.rows, units, 1, MT, KS);
     int *ex = reinterpret_cast<int *>(lds + o.ex);
     const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4;
     MvBlock<1> first;
     const int64_t n = (int64_t)16 * t0 + l;
-    load_block<1>(first, &a.w, n < a.N ? n : a.N - 1, wave_in_group(), units, a.K, g);
-    stage_rows<FMT>(lds, ex, a.x, rows, units, a.K, [&](int r) { return (int64_t)m0 + r; });
+    load_block<1, KS>(first, &a.w, n < a.N ? n : a.N - 1, first_unit<KS>(), units, a.K, g);
+    stage_rows<FMT, 64 * mv_waves(KS)>(lds, ex, a.x, rows, units, a.K, [&](int r) { return (int64_t)m0 + r; });
     __syncthreads();
-    run_tiles<1, MT>(&a.w, 0, a.N, a.K, a.tiles, t0, a.wgs_n, lds, ex, rows, units,
+    run_tiles<1, MT, KS>(&a.w, 0, a.N, a.K, a.tiles, t0, a.wgs_n * (KS == 1 ? mv_waves(1) : 1), lds, ex, rows, units,
                      reinterpret_cast<float *>(lds + o.red), reinterpret_cast<int *>(lds + o.red_e),
                      first, [&](int m, int64_t nn, const float *s, int e) {
-                         float v = s[0] * a.scales[nn / a.rows_per_scale];
+                         float v = s[0] * a.scales[udiv((uint32_t)nn, a.per_scale)];
                          if constexpr (FMT == MXQ_X_NVFP4)
                              v *= a.x.s[m0 + m];
                          st_elem<BF16_OUT>(a.c, (m0 + m) * a.N + nn, __builtin_ldexpf(v, e));
@@ -380,19 +443,19 @@ __device__ __forceinline__ bool find_segment(const int64_t *off, int n_groups, i
     return false;
 }
 
-template <bool BF16_OUT, int FMT, int MT, bool GATED>
-__global__ void __launch_bounds__(MV_THREADS) nvfp4_expert_kernel(MvArgs a)
+template <bool BF16_OUT, int FMT, int MT, int KS, bool GATED>
+__global__ void __launch_bounds__(64 * mv_waves(KS)) nvfp4_expert_kernel(MvArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int NW = GATED ? 2 : 1;
     const int units = (int)((a.K + MV_UNIT - 1) / MV_UNIT);
-    const int t0 = (int)(wg_id() % (uint32_t)a.wgs_n);
+    const int t0 = first_tile<KS>((int)(wg_id() % (uint32_t)a.wgs_n));
     int e = 0;
     int64_t r0 = 0, r1 = 0;
     if (!find_segment(a.seg_offsets, a.n_groups, a.total_rows, (int)(wg_id() / (uint32_t)a.wgs_n),
                       &e, &r0, &r1))
         return;
-    const MvLds o = mv_lds(a.chunk_rows, units, NW, MT);
+    const MvLds o = mv_lds(a.chunk_rows, units, NW, MT, KS);
     int *ex = reinterpret_cast<int *>(lds + o.ex);
     const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4;
     const WeightB w[2] = {a.w, a.up};
@@ -409,12 +472,14 @@ __global__ void __launch_bounds__(MV_THREADS) nvfp4_expert_kernel(MvArgs a)
             return x;
         };
         MvBlock<NW> first;
-        load_block<NW>(first, w, row0 + (n < a.N ? n : a.N - 1), wave_in_group(), units, a.K, g);
+        load_block<NW, KS>(first, w, row0 + (n < a.N ? n : a.N - 1), first_unit<KS>(), units, a.K,
+                           g);
         if (c0 != r0)
             __syncthreads();                      // the last chunk's rows have been read
-        stage_rows<FMT>(lds, ex, a.x, rows, units, a.K, src);
+        stage_rows<FMT, 64 * mv_waves(KS)>(lds, ex, a.x, rows, units, a.K, src);
         __syncthreads();
-        run_tiles<NW, MT>(w, row0, a.N, a.K, a.tiles, t0, a.wgs_n, lds, ex, rows, units,
+        run_tiles<NW, MT, KS>(w, row0, a.N, a.K, a.tiles, t0, a.wgs_n * (KS == 1 ? mv_waves(1) : 1),
+                              lds, ex, rows, units,
                           reinterpret_cast<float *>(lds + o.red),
                           reinterpret_cast<int *>(lds + o.red_e), first,
                           [&](int m, int64_t nn, const float *s, int ee) {
@@ -431,13 +496,22 @@ __global__ void __launch_bounds__(MV_THREADS) nvfp4_expert_kernel(MvArgs a)
 
 // Rows staged at once: at most `want`, as LDS holds them beside the partial
 // tiles of nw weights (one row of the largest K always fits).
-int staged_rows(int64_t want, int64_t K, int nw)
+int staged_rows(int64_t want, int64_t K, int nw, int ks)
 {
     const int units = (int)((K + MV_UNIT - 1) / MV_UNIT);
     int r = (int)(want < MV_MAX_ROWS ? want : MV_MAX_ROWS);
-    while (r > 1 && mv_lds(r, units, nw, (r + 15) / 16).bytes > MV_LDS)
+    while (r > 1 && mv_lds(r, units, nw, (r + 15) / 16, ks).bytes > MV_LDS)
         r--;
     return r;
+}
+
+// Workgroups that the chip's 256 compute units hold with `lds` bytes each, at
+// most MV_CU_WAVES wavefronts a unit: a launch of about as many stages its activations
+// least often (32 x 8192 x 4096: 44 us with 512 workgroups, 68 us with 1024).
+int64_t resident_target(size_t lds, int ks)
+{
+    const int64_t per_cu = MV_LDS / (int64_t)lds, most = MV_CU_WAVES / mv_waves(ks);
+    return 256 * (per_cu < 1 ? 1 : per_cu > most ? most : per_cu);
 }
 
 template <typename F>
@@ -467,27 +541,32 @@ hipError_t launch_nvfp4_matvec(const ActX &x, const WeightB &b, const float *sca
     a.x = x;
     a.w = b;
     a.scales = scales;
-    a.rows_per_scale = rows_per_scale;
+    a.per_scale = make_div((uint32_t)(rows_per_scale < N ? rows_per_scale : N));
     a.N = N;
     a.K = K;
     a.M = (int)M;
-    const int most = staged_rows(M, K, 1);
+    a.tiles = (int)((N + 15) / 16);
+    a.c = c;
+    const int ks = a.tiles >= MV_WHOLE_K_TILES ? 1 : 4;
+    const int most = staged_rows(M, K, 1, ks);
     a.passes = (int)((M + most - 1) / most);
     a.rows = (int)((M + a.passes - 1) / a.passes);
-    a.tiles = (int)((N + 15) / 16);
-    const int64_t share = MV_TARGET_WGS / a.passes < 1 ? 1 : MV_TARGET_WGS / a.passes;
-    a.wgs_n = (int)(a.tiles < share ? a.tiles : share);
-    a.c = c;
     const int mt = (a.rows + 15) / 16, units = (int)((K + MV_UNIT - 1) / MV_UNIT);
-    const size_t lds = (size_t)mv_lds(a.rows, units, 1, mt).bytes;
-    const dim3 grid((unsigned)(a.wgs_n * a.passes)), block(MV_THREADS);
+    const size_t lds = (size_t)mv_lds(a.rows, units, 1, mt, ks).bytes;
+    const int64_t work = ks == 1 ? (a.tiles + mv_waves(1) - 1) / mv_waves(1) : a.tiles;
+    const int64_t share = (resident_target(lds, ks) + a.passes - 1) / a.passes;
+    a.wgs_n = (int)(work < share ? work : share);
+    const dim3 grid((unsigned)(a.wgs_n * a.passes)), block(64 * mv_waves(ks));
     with_format(x.fmt, bf16_out, [&](auto out, auto fmt) {
         constexpr bool OUT = decltype(out)::value;
         constexpr int FMT = decltype(fmt)::value;
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, stream, a); };
         if (mt == 1)
-            hipLaunchKernelGGL((nvfp4_matvec_kernel<OUT, FMT, 1>), grid, block, lds, stream, a);
+            ks == 1 ? go(nvfp4_matvec_kernel<OUT, FMT, 1, 1>)
+                    : go(nvfp4_matvec_kernel<OUT, FMT, 1, 4>);
         else
-            hipLaunchKernelGGL((nvfp4_matvec_kernel<OUT, FMT, 2>), grid, block, lds, stream, a);
+            ks == 1 ? go(nvfp4_matvec_kernel<OUT, FMT, 2, 1>)
+                    : go(nvfp4_matvec_kernel<OUT, FMT, 2, 4>);
     });
     return hipGetLastError();
 }
@@ -517,30 +596,37 @@ hipError_t launch_nvfp4_expert_matvec(const ActX &x, int64_t n_tokens, const int
     a.n_groups = (int)n_groups;
     a.tiles = (int)((N + 15) / 16);
     a.c = c;
-    // One slot per expert that can have rows, each shared by enough workgroups that the
-    // launch has about MV_TARGET_WGS.
+    // One slot per expert that can have rows.  Rows staged at once: three even shares,
+    // which few experts exceed (they take their weights twice, from L2).
     const int64_t slots = n_groups < total_rows ? n_groups : total_rows;
-    int64_t per = (MV_TARGET_WGS + slots - 1) / slots;
-    a.wgs_n = (int)(a.tiles < per ? a.tiles : per);
-    // Rows staged at once: twice an even share of the rows (a fuller expert takes more
-    // chunks), 16 at least.
-    const int64_t even = 2 * ((total_rows + slots - 1) / slots);
+    const int64_t even = 3 * ((total_rows + slots - 1) / slots);
     const bool gated = up.codes != nullptr;
-    a.chunk_rows = staged_rows(total_rows < 16 ? total_rows : even < 16 ? 16 : even, K,
-                               gated ? 2 : 1);
+    const int nw = gated ? 2 : 1, ks = slots * a.tiles >= MV_WHOLE_K_TILES ? 1 : 4;
+    a.chunk_rows = staged_rows(total_rows < even ? total_rows : even, K, nw, ks);
     const int mt = (a.chunk_rows + 15) / 16, units = (int)((K + MV_UNIT - 1) / MV_UNIT);
-    const size_t lds = (size_t)mv_lds(a.chunk_rows, units, gated ? 2 : 1, mt).bytes;
-    const dim3 grid((unsigned)(a.wgs_n * slots)), block(MV_THREADS);
+    const size_t lds = (size_t)mv_lds(a.chunk_rows, units, nw, mt, ks).bytes;
+    // Equal shares of an expert's tiles, for about as many workgroups as fit the chip.
+    const int64_t target = resident_target(lds, ks), per = (target + slots - 1) / slots;
+    const int64_t work = ks == 1 ? (a.tiles + mv_waves(1) - 1) / mv_waves(1) : a.tiles;
+    const int64_t each = work <= per ? 1 : (work + per - 1) / per;
+    a.wgs_n = (int)((work + each - 1) / each);
+    const dim3 grid((unsigned)(a.wgs_n * slots)), block(64 * mv_waves(ks));
     with_format(x.fmt, bf16_out, [&](auto out, auto fmt) {
         constexpr bool OUT = decltype(out)::value;
         constexpr int FMT = decltype(fmt)::value;
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, stream, a); };
+        auto by_split = [&](auto mtc, auto gate) {
+            constexpr int MT = decltype(mtc)::value;
+            constexpr bool GATED = decltype(gate)::value;
+            ks == 1 ? go(nvfp4_expert_kernel<OUT, FMT, MT, 1, GATED>)
+                    : go(nvfp4_expert_kernel<OUT, FMT, MT, 4, GATED>);
+        };
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
         if (mt == 1)
-            gated ? go(nvfp4_expert_kernel<OUT, FMT, 1, true>)
-                  : go(nvfp4_expert_kernel<OUT, FMT, 1, false>);
+            gated ? by_split(One{}, std::true_type{}) : by_split(One{}, std::false_type{});
         else
-            gated ? go(nvfp4_expert_kernel<OUT, FMT, 2, true>)
-                  : go(nvfp4_expert_kernel<OUT, FMT, 2, false>);
+            gated ? by_split(Two{}, std::true_type{}) : by_split(Two{}, std::false_type{});
     });
     return hipGetLastError();
 }
