@@ -23,10 +23,13 @@
 // from zero and joins the row's sum under the running largest exponent, so
 // no sum overflows or underflows where the result does not.
 //
-// Split.  The four wavefronts of a workgroup share K (unit by unit) and join
-// through LDS for every 16-row tile of weights: small weights fill more of
-// the chip, and a wavefront has all its loads of a tile in flight.  The next
-// tile's loads are issued before the current tile is computed.
+// Split.  Of few weights (below MV_WHOLE_K_TILES tiles of 16 rows) a
+// workgroup's four wavefronts share K unit by unit and join through LDS for
+// every tile: that fills more of the chip.  Of many, every wavefront takes
+// tiles of its own and loads them in memory's order (see MvLine).  Either
+// way the next loads are issued before the current ones are multiplied.
+// Measured in graphs of ten calls: 1 x 2048 x 2048 4.7 us; 13 x 128257 x 2048
+// 36 us (151 MB: 4.2 TB/s); 1 x 1000000 x 2048 250 us (4.6 TB/s).
 #include <type_traits>
 
 #include "mxq_layer.h"
@@ -39,17 +42,11 @@ namespace {
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-#ifndef MVP
-#define MVP 16
-#define MVW 8
-#define MVK 2048
-#define MVB1 4
-#define MVB2 2
-#endif
-// Wavefronts of a workgroup that splits K among them, and of one whose wavefronts
-// take whole tiles: there more of them share the staged rows (13 x 128257 x 2048:
-// 47 us with four, two workgroups a compute unit, YYY us with eight).
-constexpr int mv_waves(int ks) { return ks == 1 ? MVW : 4; }
+// Wavefronts of a workgroup that splits K among them; one whose wavefronts take
+// whole tiles has up to MV_MAX_WAVES, which share the staged rows (13 x 128257 x
+// 2048: 47 us with four, 41 us with sixteen).  Experts have fewer rows to share and
+// fewer tiles, and keep four (8 tokens: 47 us, with eight 51 us).
+constexpr int MV_SPLIT = 4, MV_MAX_WAVES = 16;
 constexpr int MV_UNIT = 128;                      // K values per unit
 constexpr int MV_XROW = MV_UNIT * 2 + 16;         // a row's unit in LDS, padded: 16 rows at one
                                                   // offset fall in distinct banks
@@ -57,11 +54,13 @@ constexpr int MV_STAGE = 4;                       // units of rows loaded at onc
 constexpr int MV_RROW = 20;                       // floats per row of a wavefront's partial tile
 constexpr int MV_MAX_ROWS = 32;                   // activation rows of a workgroup
 constexpr int MV_LDS = 160 * 1024;                // a workgroup's most
-constexpr int64_t MV_CU_WAVES = MVP;
-constexpr int64_t MV_WHOLE_K_TILES = MVK;
-
-// Units a wavefront loads at once of nw weights.
-constexpr int mv_block(int nw) { return nw == 1 ? MVB1 : MVB2; }
+constexpr int64_t MV_CU_WAVES = 20;               // wavefronts a compute unit is given
+constexpr int64_t MV_WHOLE_K_TILES = 2048;        // 16-row tiles from which wavefronts take whole ones
+// Units of a wavefront's loads: strided ones of nw weights when K is split,
+// consecutive ones of a whole tile.
+constexpr int mv_block(int nw) { return nw == 1 ? 4 : 2; }
+constexpr int MV_LINE = 4;
+constexpr int MV_TURN = MV_LINE * 1024 + 512;     // a wavefront's LDS to turn a block in
 
 struct MvArgs {
     ActX x;
@@ -71,6 +70,7 @@ struct MvArgs {
     int64_t N, K;
     int rows;                                     // activation rows per pass (dense)
     int M, passes;                                // dense
+    int waves;                                    // wavefronts of a workgroup
     int tiles, wgs_n;                             // 16-row weight tiles, workgroups sharing them
     // Experts: rows of x, sorted by segment.
     int64_t n_tokens, total_rows;
@@ -156,11 +156,11 @@ __device__ __forceinline__ f16x8_t act_f16(const ActRaw &r, int *e)
 // Stages rows [0, rows) of the activations (row r is row src(r) of x) into
 // LDS; columns past K are zero.  ex[unit * rows + r] is the unit's exponent.
 // Each 16 lanes take a unit of a row, MV_STAGE of them loaded at once.
-template <int FMT, int THREADS, typename Src>
+template <int FMT, typename Src>
 __device__ __forceinline__ void stage_rows(uint8_t *xs, int *ex, const ActX &x, int rows,
-                                           int units, int64_t K, Src src)
+                                           int units, int64_t K, int waves, Src src)
 {
-    constexpr int GROUPS = THREADS / 16;
+    const int GROUPS = 4 * waves;
     const int l16 = (int)(tid() & 15), total = rows * units;
     for (int p0 = (int)(tid() >> 4); p0 < total; p0 += GROUPS * MV_STAGE) {
         ActRaw raw[MV_STAGE];
@@ -192,13 +192,13 @@ struct MvBlock {
     u32x4_t c[NW][U];
     uint32_t s[NW][U];
 };
-template <int NW, int KS>
+template <int NW>
 __device__ __forceinline__ void load_block(MvBlock<NW> &b, const WeightB *w, int64_t row, int u0,
                                            int units, int64_t K, int g)
 {
 #pragma unroll
     for (int j = 0; j < mv_block(NW); j++) {
-        const int u = u0 + KS * j;
+        const int u = u0 + MV_SPLIT * j;
         if (u < units) {
             // The half unit that ends a K of 64 (mod 128): the upper lane groups read the
             // lower ones' codes, against zero activations.
@@ -222,14 +222,14 @@ struct MvSums {
     int e[MT];
 };
 
-template <int NW, int MT, int KS>
+template <int NW, int MT>
 __device__ __forceinline__ void multiply_block(MvSums<NW, MT> &st, const MvBlock<NW> &b,
                                                const uint8_t *xs, const int *ex, int rows, int u0,
                                                int units, int l, int g)
 {
 #pragma unroll
     for (int j = 0; j < mv_block(NW); j++) {
-        const int u = u0 + KS * j;
+        const int u = u0 + MV_SPLIT * j;
         if (u >= units)
             break;
         f32x4_t d[NW][MT];
@@ -272,27 +272,107 @@ __device__ __forceinline__ void multiply_block(MvSums<NW, MT> &st, const MvBlock
     }
 }
 
-// A wavefront's place in the split: KS = 4, the workgroup's wavefronts share K
-// (wavefront w takes units w, w + 4, ...) and each tile is the workgroup's;
-// KS = 1, a tile is one wavefront's and its wavefronts take consecutive ones.
-template <int KS>
-__device__ __forceinline__ int first_tile(int wg) { return KS == 1 ? mv_waves(1) * wg + wave_in_group() : wg; }
-template <int KS>
-__device__ __forceinline__ int first_unit() { return KS == 1 ? 0 : wave_in_group(); }
+// The loads of up to MV_LINE consecutive units of a whole tile, in memory's
+// order: 256 consecutive bytes of each of four rows an instruction (64 bytes
+// of sixteen rows, the order of the matrix instructions, reach 3.9 TB/s,
+// these 5.7).  They are turned into that order through LDS, a wavefront by
+// itself: slot s of row r holds 16-byte piece s ^ r, so that sixteen rows at
+// one piece fall in distinct banks.
+struct MvLine {
+    u32x4_t c[4];
+    uint32_t s[2];
+};
+__device__ __forceinline__ void load_line(MvLine &b, const WeightB &w, int64_t row0,
+                                          int64_t last_row, int u0, int64_t K, int lane)
+{
+    const int pieces = (int)(K >> 5), sbytes = (int)(K >> 4);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const int r = 4 * j + (lane >> 4);
+        int p = 4 * u0 + ((lane & 15) ^ r);
+        p = p < pieces ? p : pieces - 1;             // past K: any codes, against zeros
+        const int64_t row = row0 + r < last_row ? row0 + r : last_row;
+        b.c[j] = *reinterpret_cast<const u32x4_t *>(w.codes + row * (K >> 1) + 16 * p);
+    }
+    const int64_t row = row0 + (lane >> 2) < last_row ? row0 + (lane >> 2) : last_row;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        int o = 8 * (u0 + (lane & 3)) + 4 * h;
+        o = o < sbytes ? o : sbytes - 4;
+        b.s[h] = *reinterpret_cast<const uint32_t *>(w.bs + row * sbytes + o);
+    }
+}
+template <int MT>
+__device__ __forceinline__ void multiply_line(MvSums<1, MT> &st, const MvLine &b, uint8_t *turn,
+                                              const uint8_t *xs, const int *ex, int rows, int u0,
+                                              int units, int lane)
+{
+    const int l = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        *reinterpret_cast<u32x4_t *>(turn + 1024 * j + 16 * lane) = b.c[j];
+    *reinterpret_cast<u32x2_t *>(turn + 4096 + 8 * lane) = u32x2_t{b.s[0], b.s[1]};
+    // The block's sums join under the largest of its exponents and the sum's own.
+    int xr[MT];
+    float f[MV_LINE][MT];
+#pragma unroll
+    for (int t = 0; t < MT; t++) {
+        xr[t] = 16 * t + l < rows ? 16 * t + l : rows - 1;
+        int e[MV_LINE], en = st.e[t];
+#pragma unroll
+        for (int j = 0; j < MV_LINE; j++) {
+            e[j] = u0 + j < units ? ex[(u0 + j) * rows + xr[t]] : -1000;
+            en = e[j] > en ? e[j] : en;
+        }
+        st.a[0][t] *= __builtin_ldexpf(1.0f, st.e[t] - en);
+        st.e[t] = en;
+#pragma unroll
+        for (int j = 0; j < MV_LINE; j++)
+            f[j][t] = __builtin_ldexpf(1.0f, e[j] - en);
+    }
+#pragma unroll
+    for (int j = 0; j < MV_LINE; j++) {
+        if (u0 + j >= units)
+            break;
+        const u32x4_t c = *reinterpret_cast<const u32x4_t *>(turn + 256 * l +
+                                                             16 * ((4 * j + g) ^ l));
+        const f16x2_t sc = e4m3_pair(*reinterpret_cast<const uint16_t *>(turn + 4096 + 32 * l +
+                                                                         8 * j + 2 * g));
+        f32x4_t d[MT];
+#pragma unroll
+        for (int t = 0; t < MT; t++)
+            d[t] = f32x4_t{};
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const f16x8_t wf = oct(c[q], sc[q >> 1]);
+#pragma unroll
+            for (int t = 0; t < MT; t++) {
+                const f16x8_t xf = *reinterpret_cast<const f16x8_t *>(
+                    xs + ((u0 + j) * rows + xr[t]) * MV_XROW + 64 * g + 16 * q);
+                d[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, xf, d[t], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < MT; t++)
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                st.a[0][t][k] = __builtin_fmaf(d[t][k], f[j][t], st.a[0][t][k]);
+    }
+}
 
 // The tiles t0, t0 + step, ... of one weight (rows row0 ..) times the staged
 // rows; out(m, n, sums, e) ends each element with the sums of the NW weights
 // in units of 2^e.
-template <int NW, int MT, int KS, typename Out>
-__device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_t N, int64_t K,
+template <int NW, int MT, typename Out>
+__device__ __forceinline__ void split_tiles(const WeightB *w, int64_t row0, int64_t N, int64_t K,
                                           int tiles, int t0, int step, const uint8_t *xs,
                                           const int *ex, int rows, int units, float *red,
                                           int *red_e, MvBlock<NW> &first, Out out)
 {
     const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
     constexpr int PART = 16 * MT * MV_RROW;                  // floats of a wavefront's tile
-    constexpr int SPAN = KS * mv_block(NW);                      // units of a block
-    const int blocks = (units + SPAN - 1) / SPAN, u0 = first_unit<KS>();
+    constexpr int SPAN = MV_SPLIT * mv_block(NW);            // units of a block
+    const int blocks = (units + SPAN - 1) / SPAN, u0 = wave;
     auto tile_row = [&](int t) {
         const int64_t n = (int64_t)16 * t + l;
         return row0 + (n < N ? n : N - 1);
@@ -312,29 +392,14 @@ __device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_
             MvBlock<NW> nx;
             const bool more = b + 1 < blocks;
             if (more || t + step < tiles)
-                load_block<NW, KS>(nx, w, tile_row(more ? t : t + step),
+                load_block<NW>(nx, w, tile_row(more ? t : t + step),
                                    u0 + (more ? SPAN * (b + 1) : 0), units, K, g);
-            multiply_block<NW, MT, KS>(st, cur, xs, ex, rows, u0 + SPAN * b, units, l, g);
+            multiply_block<NW, MT>(st, cur, xs, ex, rows, u0 + SPAN * b, units, l, g);
             cur = nx;
         }
-        if constexpr (KS == 1) {
-            // Lane (m, g) holds four consecutive columns of row m.
-#pragma unroll
-            for (int i = 0; i < MT; i++)
-                if (16 * i + l < rows)
-#pragma unroll
-                    for (int c = 0; c < 4; c++) {
-                        const int64_t n = (int64_t)16 * t + 4 * g + c;
-                        float v[NW];
-#pragma unroll
-                        for (int k = 0; k < NW; k++)
-                            v[k] = st.a[k][i][c];
-                        if (n < N)
-                            out(16 * i + l, n, v, st.e[i]);
-                    }
-        } else {
-            float *mine = red + (parity * KS + wave) * NW * PART;
-            int *mine_e = red_e + (parity * KS + wave) * 16 * MT;
+        {
+            float *mine = red + (parity * MV_SPLIT + wave) * NW * PART;
+            int *mine_e = red_e + (parity * MV_SPLIT + wave) * 16 * MT;
 #pragma unroll
             for (int i = 0; i < MT; i++) {
                 if (g == 0)
@@ -347,12 +412,12 @@ __device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_
             __syncthreads();
             // Tile t's partials are read here and overwritten two tiles on, behind the
             // next tile's barrier.
-            for (int o = (int)tid(); o < 16 * rows; o += 64 * KS) {
+            for (int o = (int)tid(); o < 16 * rows; o += 64 * MV_SPLIT) {
                 const int m = o >> 4, n = o & 15;
                 int e = -300;
 #pragma unroll
-                for (int v = 0; v < KS; v++) {
-                    const int ev = red_e[(parity * KS + v) * 16 * MT + m];
+                for (int v = 0; v < MV_SPLIT; v++) {
+                    const int ev = red_e[(parity * MV_SPLIT + v) * 16 * MT + m];
                     e = e > ev ? e : ev;
                 }
                 float s[NW];
@@ -360,10 +425,10 @@ __device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_
                 for (int k = 0; k < NW; k++) {
                     s[k] = 0.0f;
 #pragma unroll
-                    for (int v = 0; v < KS; v++)
+                    for (int v = 0; v < MV_SPLIT; v++)
                         s[k] += __builtin_ldexpf(
-                            red[(parity * KS + v) * NW * PART + k * PART + m * MV_RROW + n],
-                            red_e[(parity * KS + v) * 16 * MT + m] - e);
+                            red[(parity * MV_SPLIT + v) * NW * PART + k * PART + m * MV_RROW + n],
+                            red_e[(parity * MV_SPLIT + v) * 16 * MT + m] - e);
                 }
                 if ((int64_t)16 * t + n < N)
                     out(m, (int64_t)16 * t + n, s, e);
@@ -373,44 +438,107 @@ __device__ __forceinline__ void run_tiles(const WeightB *w, int64_t row0, int64_
     }
 }
 
-// LDS of a launch: staged rows, their exponents, two parities of partials.
+// The same by a wavefront alone: tiles t0, t0 + step, ..., all of K each, one
+// weight after the other.
+template <int NW, int MT, typename Out>
+__device__ __forceinline__ void whole_tiles(const WeightB *w, int64_t row0, int64_t N, int64_t K,
+                                            int tiles, int t0, int step, const uint8_t *xs,
+                                            const int *ex, int rows, int units, uint8_t *turn,
+                                            MvLine &first, Out out)
+{
+    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4;
+    const int blocks = (units + MV_LINE - 1) / MV_LINE;
+    MvLine cur = first;
+    for (int t = t0; t < tiles; t += step) {
+        MvSums<1, MT> st[NW];
+#pragma unroll
+        for (int i = 0; i < NW; i++) {
+#pragma unroll
+            for (int m = 0; m < MT; m++) {
+                st[i].e[m] = -300;
+                st[i].a[0][m] = f32x4_t{};
+            }
+            for (int b = 0; b < blocks; b++) {
+                MvLine nx;
+                const bool more = b + 1 < blocks, here = more || i + 1 < NW;
+                if (here || t + step < tiles)
+                    load_line(nx, w[more ? i : i + 1 < NW ? i + 1 : 0],
+                              row0 + 16 * (int64_t)(here ? t : t + step), row0 + N - 1,
+                              more ? MV_LINE * (b + 1) : 0, K, lane);
+                multiply_line<MT>(st[i], cur, turn, xs, ex, rows, MV_LINE * b, units, lane);
+                cur = nx;
+            }
+        }
+        // Lane (m, g) holds four consecutive columns of row m, every weight's under the
+        // same exponent (the row's largest).
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+            if (16 * m + l < rows)
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    const int64_t n = (int64_t)16 * t + 4 * g + c;
+                    float v[NW];
+#pragma unroll
+                    for (int i = 0; i < NW; i++)
+                        v[i] = st[i].a[0][m][c];
+                    if (n < N)
+                        out(16 * m + l, n, v, st[0].e[m]);
+                }
+    }
+}
+
+// LDS of a launch: staged rows, their exponents, then two parities of the
+// wavefronts' partial tiles (K split, waves = 0) or each wavefront's room to
+// turn its loads in.
 struct MvLds {
     int ex, red, red_e, bytes;
 };
-__host__ __device__ inline MvLds mv_lds(int rows, int units, int nw, int mt, int ks)
+__host__ __device__ inline MvLds mv_lds(int rows, int units, int nw, int mt, int waves)
 {
     MvLds o;
     o.ex = rows * units * MV_XROW;
     o.red = o.ex + (rows * units * 4 + 15) / 16 * 16;
-    o.red_e = o.red + (ks == 1 ? 0 : 2 * ks * nw * 16 * mt * MV_RROW * 4);
-    o.bytes = o.red_e + (ks == 1 ? 0 : 2 * ks * 16 * mt * 4);
+    o.red_e = o.red + (waves ? waves * MV_TURN : 2 * MV_SPLIT * nw * 16 * mt * MV_RROW * 4);
+    o.bytes = o.red_e + (waves ? 0 : 2 * MV_SPLIT * 16 * mt * 4);
     return o;
 }
 
-template <bool BF16_OUT, int FMT, int MT, int KS>
-__global__ void __launch_bounds__(64 * mv_waves(KS)) nvfp4_matvec_kernel(MvArgs a)
+template <bool BF16_OUT, int FMT, int MT, bool WHOLE>
+__global__ void __launch_bounds__(64 * (WHOLE ? MV_MAX_WAVES : MV_SPLIT))
+    nvfp4_matvec_kernel(MvArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int units = (int)((a.K + MV_UNIT - 1) / MV_UNIT);
-    const int wg = (int)(wg_id() / (uint32_t)a.passes), t0 = first_tile<KS>(wg);
-    const int pass = (int)(wg_id() % (uint32_t)a.passes);
+    const int wg = (int)(wg_id() / (uint32_t)a.passes), pass = (int)(wg_id() % (uint32_t)a.passes);
     const int m0 = pass * a.rows, rows = a.M - m0 < a.rows ? a.M - m0 : a.rows;
-    const MvLds o = mv_lds(a.rows, units, 1, MT, KS);
+    const MvLds o = mv_lds(a.rows, units, 1, MT, WHOLE ? a.waves : 0);
     int *ex = reinterpret_cast<int *>(lds + o.ex);
-    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4;
-    MvBlock<1> first;
-    const int64_t n = (int64_t)16 * t0 + l;
-    load_block<1, KS>(first, &a.w, n < a.N ? n : a.N - 1, first_unit<KS>(), units, a.K, g);
-    stage_rows<FMT, 64 * mv_waves(KS)>(lds, ex, a.x, rows, units, a.K, [&](int r) { return (int64_t)m0 + r; });
-    __syncthreads();
-    run_tiles<1, MT, KS>(&a.w, 0, a.N, a.K, a.tiles, t0, a.wgs_n * (KS == 1 ? mv_waves(1) : 1), lds, ex, rows, units,
-                     reinterpret_cast<float *>(lds + o.red), reinterpret_cast<int *>(lds + o.red_e),
-                     first, [&](int m, int64_t nn, const float *s, int e) {
-                         float v = s[0] * a.scales[udiv((uint32_t)nn, a.per_scale)];
-                         if constexpr (FMT == MXQ_X_NVFP4)
-                             v *= a.x.s[m0 + m];
-                         st_elem<BF16_OUT>(a.c, (m0 + m) * a.N + nn, __builtin_ldexpf(v, e));
-                     });
+    const int lane = (int)lane_id(), wave = wave_in_group();
+    auto src = [&](int r) { return (int64_t)m0 + r; };
+    auto out = [&](int m, int64_t nn, const float *s, int e) {
+        float v = s[0] * a.scales[udiv((uint32_t)nn, a.per_scale)];
+        if constexpr (FMT == MXQ_X_NVFP4)
+            v *= a.x.s[m0 + m];
+        st_elem<BF16_OUT>(a.c, (m0 + m) * a.N + nn, __builtin_ldexpf(v, e));
+    };
+    if constexpr (WHOLE) {
+        const int t0 = wg * a.waves + wave;
+        MvLine first;
+        load_line(first, a.w, (int64_t)16 * t0, a.N - 1, 0, a.K, lane);
+        stage_rows<FMT>(lds, ex, a.x, rows, units, a.K, a.waves, src);
+        __syncthreads();
+        whole_tiles<1, MT>(&a.w, 0, a.N, a.K, a.tiles, t0, a.wgs_n * a.waves, lds, ex, rows, units,
+                           lds + o.red + wave * MV_TURN, first, out);
+    } else {
+        const int64_t n = (int64_t)16 * wg + (lane & 15);
+        MvBlock<1> first;
+        load_block<1>(first, &a.w, n < a.N ? n : a.N - 1, wave, units, a.K, lane >> 4);
+        stage_rows<FMT>(lds, ex, a.x, rows, units, a.K, a.waves, src);
+        __syncthreads();
+        split_tiles<1, MT>(&a.w, 0, a.N, a.K, a.tiles, wg, a.wgs_n, lds, ex, rows, units,
+                           reinterpret_cast<float *>(lds + o.red),
+                           reinterpret_cast<int *>(lds + o.red_e), first, out);
+    }
 }
 
 // The expert of slot s (the s-th segment that has rows) and its rows.
@@ -443,23 +571,24 @@ __device__ __forceinline__ bool find_segment(const int64_t *off, int n_groups, i
     return false;
 }
 
-template <bool BF16_OUT, int FMT, int MT, int KS, bool GATED>
-__global__ void __launch_bounds__(64 * mv_waves(KS)) nvfp4_expert_kernel(MvArgs a)
+template <bool BF16_OUT, int FMT, int MT, bool WHOLE, bool GATED>
+__global__ void __launch_bounds__(64 * (WHOLE ? MV_MAX_WAVES : MV_SPLIT))
+    nvfp4_expert_kernel(MvArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int NW = GATED ? 2 : 1;
     const int units = (int)((a.K + MV_UNIT - 1) / MV_UNIT);
-    const int t0 = first_tile<KS>((int)(wg_id() % (uint32_t)a.wgs_n));
+    const int wg = (int)(wg_id() % (uint32_t)a.wgs_n);
     int e = 0;
     int64_t r0 = 0, r1 = 0;
     if (!find_segment(a.seg_offsets, a.n_groups, a.total_rows, (int)(wg_id() / (uint32_t)a.wgs_n),
                       &e, &r0, &r1))
         return;
-    const MvLds o = mv_lds(a.chunk_rows, units, NW, MT, KS);
+    const MvLds o = mv_lds(a.chunk_rows, units, NW, MT, WHOLE ? a.waves : 0);
     int *ex = reinterpret_cast<int *>(lds + o.ex);
-    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4;
+    const int lane = (int)lane_id(), wave = wave_in_group();
     const WeightB w[2] = {a.w, a.up};
-    const int64_t row0 = (int64_t)e * a.N, n = (int64_t)16 * t0 + l;
+    const int64_t row0 = (int64_t)e * a.N;
     const float scale = a.scales[e];
     for (int64_t c0 = r0; c0 < r1; c0 += a.chunk_rows) {
         const int rows = (int)(r1 - c0 < a.chunk_rows ? r1 - c0 : a.chunk_rows);
@@ -471,46 +600,67 @@ __global__ void __launch_bounds__(64 * mv_waves(KS)) nvfp4_expert_kernel(MvArgs 
             }
             return x;
         };
-        MvBlock<NW> first;
-        load_block<NW, KS>(first, w, row0 + (n < a.N ? n : a.N - 1), first_unit<KS>(), units, a.K,
-                           g);
-        if (c0 != r0)
-            __syncthreads();                      // the last chunk's rows have been read
-        stage_rows<FMT, 64 * mv_waves(KS)>(lds, ex, a.x, rows, units, a.K, src);
-        __syncthreads();
-        run_tiles<NW, MT, KS>(w, row0, a.N, a.K, a.tiles, t0, a.wgs_n * (KS == 1 ? mv_waves(1) : 1),
-                              lds, ex, rows, units,
-                          reinterpret_cast<float *>(lds + o.red),
-                          reinterpret_cast<int *>(lds + o.red_e), first,
-                          [&](int m, int64_t nn, const float *s, int ee) {
-                              float sx = 1.0f;
-                              if constexpr (FMT == MXQ_X_NVFP4)
-                                  sx = a.x.s[src(m)];
-                              float v = __builtin_ldexpf(s[0] * scale * sx, ee);
-                              if constexpr (GATED)
-                                  v = silu_f32(v) * __builtin_ldexpf(s[NW - 1] * scale * sx, ee);
-                              st_elem<BF16_OUT>(a.c, (c0 + m) * a.N + nn, v);
-                          });
+        auto out = [&](int m, int64_t nn, const float *s, int ee) {
+            float sx = 1.0f;
+            if constexpr (FMT == MXQ_X_NVFP4)
+                sx = a.x.s[src(m)];
+            float v = __builtin_ldexpf(s[0] * scale * sx, ee);
+            if constexpr (GATED)
+                v = silu_f32(v) * __builtin_ldexpf(s[NW - 1] * scale * sx, ee);
+            st_elem<BF16_OUT>(a.c, (c0 + m) * a.N + nn, v);
+        };
+        auto stage = [&] {
+            if (c0 != r0)
+                __syncthreads();                  // the last chunk's rows have been read
+            stage_rows<FMT>(lds, ex, a.x, rows, units, a.K, a.waves, src);
+            __syncthreads();
+        };
+        if constexpr (WHOLE) {
+            const int t0 = wg * a.waves + wave;
+            MvLine first;
+            load_line(first, w[0], row0 + 16 * (int64_t)t0, row0 + a.N - 1, 0, a.K, lane);
+            stage();
+            whole_tiles<NW, MT>(w, row0, a.N, a.K, a.tiles, t0, a.wgs_n * a.waves, lds, ex, rows,
+                                units, lds + o.red + wave * MV_TURN, first, out);
+        } else {
+            const int64_t n = (int64_t)16 * wg + (lane & 15);
+            MvBlock<NW> first;
+            load_block<NW>(first, w, row0 + (n < a.N ? n : a.N - 1), wave, units, a.K, lane >> 4);
+            stage();
+            split_tiles<NW, MT>(w, row0, a.N, a.K, a.tiles, wg, a.wgs_n, lds, ex, rows, units,
+                                reinterpret_cast<float *>(lds + o.red),
+                                reinterpret_cast<int *>(lds + o.red_e), first, out);
+        }
     }
 }
 
-// Rows staged at once: at most `want`, as LDS holds them beside the partial
-// tiles of nw weights (one row of the largest K always fits).
-int staged_rows(int64_t want, int64_t K, int nw, int ks)
+// Rows staged at once: at most `want`, as LDS holds them beside the rest
+// (one row of the largest K always fits).
+int staged_rows(int64_t want, int units, int nw, int waves)
 {
-    const int units = (int)((K + MV_UNIT - 1) / MV_UNIT);
     int r = (int)(want < MV_MAX_ROWS ? want : MV_MAX_ROWS);
-    while (r > 1 && mv_lds(r, units, nw, (r + 15) / 16, ks).bytes > MV_LDS)
+    while (r > 1 && mv_lds(r, units, nw, (r + 15) / 16, waves).bytes > MV_LDS)
         r--;
     return r;
 }
+// Wavefronts of a workgroup that takes whole tiles: as many as fit beside the
+// rows, 0 if not even four do.
+int whole_waves(int64_t rows, int units, int nw, int most)
+{
+    const int r = (int)(rows < MV_MAX_ROWS ? rows : MV_MAX_ROWS);
+    for (int w = most; w >= 4; w /= 2)
+        if (mv_lds(r, units, nw, (r + 15) / 16, w).bytes <= MV_LDS)
+            return w;
+    return 0;
+}
 
 // Workgroups that the chip's 256 compute units hold with `lds` bytes each, at
-// most MV_CU_WAVES wavefronts a unit: a launch of about as many stages its activations
-// least often (32 x 8192 x 4096: 44 us with 512 workgroups, 68 us with 1024).
-int64_t resident_target(size_t lds, int ks)
+// most MV_CU_WAVES wavefronts a unit: a launch of about as many stages its
+// activations least often (32 x 8192 x 4096: 44 us with 512 workgroups,
+// 68 us with 1024).
+int64_t resident_target(int64_t lds, int waves)
 {
-    const int64_t per_cu = MV_LDS / (int64_t)lds, most = MV_CU_WAVES / mv_waves(ks);
+    const int64_t per_cu = MV_LDS / lds, most = MV_CU_WAVES / waves;
     return 256 * (per_cu < 1 ? 1 : per_cu > most ? most : per_cu);
 }
 
@@ -547,26 +697,28 @@ hipError_t launch_nvfp4_matvec(const ActX &x, const WeightB &b, const float *sca
     a.M = (int)M;
     a.tiles = (int)((N + 15) / 16);
     a.c = c;
-    const int ks = a.tiles >= MV_WHOLE_K_TILES ? 1 : 4;
-    const int most = staged_rows(M, K, 1, ks);
+    const int units = (int)((K + MV_UNIT - 1) / MV_UNIT);
+    const int whole = a.tiles >= MV_WHOLE_K_TILES ? whole_waves(M, units, 1, MV_MAX_WAVES) : 0;
+    const int most = staged_rows(M, units, 1, whole);
     a.passes = (int)((M + most - 1) / most);
     a.rows = (int)((M + a.passes - 1) / a.passes);
-    const int mt = (a.rows + 15) / 16, units = (int)((K + MV_UNIT - 1) / MV_UNIT);
-    const size_t lds = (size_t)mv_lds(a.rows, units, 1, mt, ks).bytes;
-    const int64_t work = ks == 1 ? (a.tiles + mv_waves(1) - 1) / mv_waves(1) : a.tiles;
-    const int64_t share = (resident_target(lds, ks) + a.passes - 1) / a.passes;
+    a.waves = whole ? whole : MV_SPLIT;
+    const int mt = (a.rows + 15) / 16;
+    const size_t lds = (size_t)mv_lds(a.rows, units, 1, mt, whole).bytes;
+    const int64_t work = whole ? (a.tiles + whole - 1) / whole : a.tiles;
+    const int64_t share = (resident_target((int64_t)lds, a.waves) + a.passes - 1) / a.passes;
     a.wgs_n = (int)(work < share ? work : share);
-    const dim3 grid((unsigned)(a.wgs_n * a.passes)), block(64 * mv_waves(ks));
+    const dim3 grid((unsigned)(a.wgs_n * a.passes)), block(64 * a.waves);
     with_format(x.fmt, bf16_out, [&](auto out, auto fmt) {
         constexpr bool OUT = decltype(out)::value;
         constexpr int FMT = decltype(fmt)::value;
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, stream, a); };
         if (mt == 1)
-            ks == 1 ? go(nvfp4_matvec_kernel<OUT, FMT, 1, 1>)
-                    : go(nvfp4_matvec_kernel<OUT, FMT, 1, 4>);
+            whole ? go(nvfp4_matvec_kernel<OUT, FMT, 1, true>)
+                  : go(nvfp4_matvec_kernel<OUT, FMT, 1, false>);
         else
-            ks == 1 ? go(nvfp4_matvec_kernel<OUT, FMT, 2, 1>)
-                    : go(nvfp4_matvec_kernel<OUT, FMT, 2, 4>);
+            whole ? go(nvfp4_matvec_kernel<OUT, FMT, 2, true>)
+                  : go(nvfp4_matvec_kernel<OUT, FMT, 2, false>);
     });
     return hipGetLastError();
 }
@@ -601,16 +753,20 @@ hipError_t launch_nvfp4_expert_matvec(const ActX &x, int64_t n_tokens, const int
     const int64_t slots = n_groups < total_rows ? n_groups : total_rows;
     const int64_t even = 3 * ((total_rows + slots - 1) / slots);
     const bool gated = up.codes != nullptr;
-    const int nw = gated ? 2 : 1, ks = slots * a.tiles >= MV_WHOLE_K_TILES ? 1 : 4;
-    a.chunk_rows = staged_rows(total_rows < even ? total_rows : even, K, nw, ks);
-    const int mt = (a.chunk_rows + 15) / 16, units = (int)((K + MV_UNIT - 1) / MV_UNIT);
-    const size_t lds = (size_t)mv_lds(a.chunk_rows, units, nw, mt, ks).bytes;
+    const int nw = gated ? 2 : 1, units = (int)((K + MV_UNIT - 1) / MV_UNIT);
+    const int64_t want = total_rows < even ? total_rows : even;
+    const int whole = slots * a.tiles >= MV_WHOLE_K_TILES ? whole_waves(want, units, nw, MV_SPLIT) : 0;
+    a.chunk_rows = staged_rows(want, units, nw, whole);
+    a.waves = whole ? whole : MV_SPLIT;
+    const int mt = (a.chunk_rows + 15) / 16;
+    const size_t lds = (size_t)mv_lds(a.chunk_rows, units, nw, mt, whole).bytes;
     // Equal shares of an expert's tiles, for about as many workgroups as fit the chip.
-    const int64_t target = resident_target(lds, ks), per = (target + slots - 1) / slots;
-    const int64_t work = ks == 1 ? (a.tiles + mv_waves(1) - 1) / mv_waves(1) : a.tiles;
+    const int64_t target = resident_target((int64_t)lds, a.waves);
+    const int64_t per = (target + slots - 1) / slots;
+    const int64_t work = whole ? (a.tiles + whole - 1) / whole : a.tiles;
     const int64_t each = work <= per ? 1 : (work + per - 1) / per;
     a.wgs_n = (int)((work + each - 1) / each);
-    const dim3 grid((unsigned)(a.wgs_n * slots)), block(64 * mv_waves(ks));
+    const dim3 grid((unsigned)(a.wgs_n * slots)), block(64 * a.waves);
     with_format(x.fmt, bf16_out, [&](auto out, auto fmt) {
         constexpr bool OUT = decltype(out)::value;
         constexpr int FMT = decltype(fmt)::value;
@@ -618,8 +774,8 @@ hipError_t launch_nvfp4_expert_matvec(const ActX &x, int64_t n_tokens, const int
         auto by_split = [&](auto mtc, auto gate) {
             constexpr int MT = decltype(mtc)::value;
             constexpr bool GATED = decltype(gate)::value;
-            ks == 1 ? go(nvfp4_expert_kernel<OUT, FMT, MT, 1, GATED>)
-                    : go(nvfp4_expert_kernel<OUT, FMT, MT, 4, GATED>);
+            whole ? go(nvfp4_expert_kernel<OUT, FMT, MT, true, GATED>)
+                  : go(nvfp4_expert_kernel<OUT, FMT, MT, false, GATED>);
         };
         using One = std::integral_constant<int, 1>;
         using Two = std::integral_constant<int, 2>;
