@@ -73,6 +73,10 @@ __device__ __forceinline__ uint32_t lane_get(uint32_t v, uint32_t src)
 {
     return (uint32_t)__builtin_amdgcn_ds_bpermute((int)(src << 2), (int)v);
 }
+__device__ __forceinline__ int lane_get(int v, uint32_t src)
+{
+    return __builtin_amdgcn_ds_bpermute((int)(src << 2), v);
+}
 __device__ __forceinline__ float lane_get(float v, uint32_t src)
 {
     return u2f(lane_get(f2u(v), src));

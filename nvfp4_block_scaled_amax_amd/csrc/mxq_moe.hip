@@ -2,8 +2,23 @@
 //
 // Route: each token's top_k experts under softmax or sigmoid scores (with an
 // optional balance bias and expert groups), their weights, and the index
-// maps of the expert-sorted layout.  The selection is that of the exact
-// scores: the order is decided in 64 bits.
+// maps of the expert-sorted layout.
+//
+// A token is worked on by L lanes (16, or 64 for many experts or choices),
+// each with V consecutive experts in registers; the next choice is a maximum
+// over them by DPP, then the lowest index among those equal to it.  The
+// selection is that of the exact scores: without a bias (and with groups
+// ranked by their best expert) scores rise with the logits, so the logits
+// themselves are compared; otherwise the keys are formed in fp32 with a bound
+// on their error, and a wavefront that finds two neighbours of the order
+// closer than the bound repeats its tokens in 64 bits.
+//
+// Maps: a tile is 64 tokens, and a 64-bit word per (tile, expert) marks the
+// tokens that chose the expert.  Bits are set with atomics, whose order
+// cannot matter, and a copy's rank is a population count, so the maps do
+// not depend on any order of execution.  One tile: the routing workgroup
+// writes them itself.  Few: a second kernel sums the tiles before its own.
+// Many: a kernel between them forms those sums, one wavefront an expert.
 #include "mxq_layer.h"
 #include "mxq_layer_device.h"
 
@@ -11,281 +26,416 @@ namespace mxq {
 
 namespace {
 
-constexpr int ROUTE_WAVES = 4;                    // tokens per workgroup, one per wavefront
-// Tokens per tile of the map kernels: 64-token words of a bit per (token,
-// expert), WORDS of them per tile.
-constexpr int MAP_WORDS = 4, MAP_TOKENS = 64 * MAP_WORDS;
-constexpr int MAP_THREADS = 256;
+constexpr int ROUTE_WAVES = 4, ROUTE_THREADS = 64 * ROUTE_WAVES;
+constexpr int MAP_TOKENS = 64;                    // tokens of a tile
+constexpr int MAP_SELF_TILES = 16;                // most tiles that sum up for themselves
 
 struct RouteArgs {
     const void *logits;
     const float *bias;
     int64_t n_tokens;
-    int n_experts, top_k, n_groups, topk_groups, group_topk;
+    int n_experts, top_k, n_groups, topk_groups, group_topk, per_group;
+    Div per_div;
     bool sigmoid, renorm;
     float scale;
     float *weights;
     int64_t *experts;
+    int64_t *token_rows, *row_tokens, *seg_offsets;     // one tile: written here
+    uint64_t *masks;                                    // [tile][expert], nullptr: no maps
 };
 
-// The larger key, of equal keys the lower index; key -inf loses to nothing
-// but another -inf.
-__device__ __forceinline__ void argmax_step(double &v, int &i, double ov, int oi)
+template <typename T>
+__device__ __forceinline__ T none();
+template <>
+__device__ __forceinline__ float none<float>() { return -__builtin_inff(); }
+template <>
+__device__ __forceinline__ double none<double>() { return -__builtin_inf(); }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_get(float v) { return u2f(dpp<CTRL>(f2u(v))); }
+template <int CTRL>
+__device__ __forceinline__ int dpp_get(int v) { return (int)dpp<CTRL>((uint32_t)v); }
+template <int CTRL>
+__device__ __forceinline__ double dpp_get(double v)
 {
-    if (ov > v || (ov == v && oi < i)) {
-        v = ov;
-        i = oi;
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 |
+                                          dpp<CTRL>((uint32_t)u));
+}
+// v and its copy from lane ^ 16 (^ 32) joined by f.
+template <int STEP, typename T, typename F>
+__device__ __forceinline__ T join_far(T v, F f)
+{
+    return f(v, lane_get(v, lane_id() ^ STEP));
+}
+// f over the L lanes of a token, the same in each.
+template <int L, typename T, typename F>
+__device__ __forceinline__ T over_lanes(T v, F f)
+{
+    v = f(v, dpp_get<DPP_XOR1>(v));
+    v = f(v, dpp_get<DPP_XOR2>(v));
+    v = f(v, dpp_get<DPP_HALF_MIRROR>(v));
+    v = f(v, dpp_get<DPP_MIRROR>(v));
+    if constexpr (L == 64) {
+        v = join_far<16>(v, f);
+        v = join_far<32>(v, f);
     }
-}
-__device__ __forceinline__ void wave_argmax(double &v, int &i, uint32_t lane)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        argmax_step(v, i, lane_get(v, lane ^ m), (int)lane_get((uint32_t)i, lane ^ m));
-}
-__device__ __forceinline__ double wave_sum_f64(double v, uint32_t lane)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        v += lane_get(v, lane ^ m);
     return v;
 }
+struct MaxOf {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a > b ? a : b; }
+};
+struct MinOf {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a < b ? a : b; }
+};
+struct SumOf {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
 
-constexpr double NONE = -__builtin_inf();
+__device__ __forceinline__ float exp_of(float x) { return exp_f32(x); }
+__device__ __forceinline__ double exp_of(double x) { return exp_f64(x); }
 
-// One wavefront routes one token; lane l holds experts l, l + 64, ...
-template <bool BF16, int V>
-__global__ void __launch_bounds__(64 * ROUTE_WAVES) moe_route_kernel(RouteArgs a)
+// The largest of the lanes' keys and its index (the lowest of equals; any
+// index if all keys are none).
+template <int L, int V, typename T>
+__device__ __forceinline__ T best_key(const T (&key)[V], int l, int *index)
 {
-    const uint32_t lane = lane_id();
-    const int64_t t = (int64_t)wg_id() * ROUTE_WAVES + wave_in_group();
-    if (t >= a.n_tokens)
-        return;
-    const int E = a.n_experts;
-    double x[V], key[V];
-    double m = NONE;
+    T m = key[0];
+#pragma unroll
+    for (int j = 1; j < V; j++)
+        m = key[j] > m ? key[j] : m;
+    m = over_lanes<L>(m, MaxOf{});
+    int i = 1 << 20;
+#pragma unroll
+    for (int j = V - 1; j >= 0; j--)
+        i = key[j] == m ? l * V + j : i;
+    *index = over_lanes<L>(i, MinOf{});
+    return m;
+}
+
+// Chooses the experts of a token from its logits x (none: never selected):
+// lane c of its L lanes gets choice c, -1 where none is left.  lds: room for the
+// keys of a token (groups).  Returns whether the keys' error leaves no doubt
+// (always in 64 bits); den is the softmax's sum under the largest logit m.
+template <int L, int V, typename T>
+__device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V],
+                                       const float (&bias)[V], int l, T *lds, int *chosen,
+                                       T *top, T *den)
+{
+    const bool by_logit = !a.bias && (a.n_groups == 1 || a.group_topk == 1);
+    T key[V], m = none<T>(), sum = 0;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-        const int e = 64 * j + (int)lane;
-        float f = -__builtin_inff();
-        if (e < E) {
-            f = ld_elem<BF16>(a.logits, t * E + e);
-            if (is_masked(f) || (a.bias && is_masked(a.bias[e])))
-                f = -__builtin_inff();
-            f = f < 3.402823466e+38f ? f : 3.402823466e+38f;
-        }
-        x[j] = (double)f;
-        m = x[j] > m ? x[j] : m;
+        key[j] = (T)x[j];
+        m = key[j] > m ? key[j] : m;
     }
-    const bool by_logit = !a.bias && (a.n_groups == 1 || a.group_topk == 1);
-    double denom = 1.0;
-    if (!a.sigmoid) {
-        int dummy = 0;
-        wave_argmax(m, dummy, lane);
-        double s = 0.0;
+    T doubt = 0;
+    if (!a.sigmoid && (!by_logit || !a.renorm)) {
+        m = over_lanes<L>(m, MaxOf{});
 #pragma unroll
         for (int j = 0; j < V; j++)
-            s += x[j] == NONE ? 0.0 : exp_f64(x[j] - m);
-        denom = wave_sum_f64(s, lane);
+            sum += key[j] == none<T>() ? (T)0 : exp_of(key[j] - m);
+        sum = over_lanes<L>(sum, SumOf{});
     }
-    auto score = [&](double v) {
-        return a.sigmoid ? 1.0 / (1.0 + exp_f64(-v)) : exp_f64(v - m) / denom;
+    *top = m;
+    *den = sum;
+    if (!by_logit) {
+        // fp32 scores are off by less than 2^-20 of the largest (exponential, sum of 1024
+        // terms, quotient), keys by another 2^-24 of their size.
+        doubt = (T)0x1p-18 * (a.sigmoid ? (T)1 : (T)1 / sum);
+#pragma unroll
+        for (int j = 0; j < V; j++)
+            if (key[j] != none<T>())
+                key[j] = (a.sigmoid ? (T)1 / ((T)1 + exp_of(-key[j])) : exp_of(key[j] - m) / sum) +
+                         (T)bias[j];
+    }
+    bool sure = true;
+    auto close_keys = [&](T hi, T lo) {
+        const T size = hi > -lo ? hi : -lo;
+        return sizeof(T) == 4 && !by_logit && lo != none<T>() &&
+               hi - lo <= doubt + (T)0x1p-20 * (size > (T)0 ? size : (T)0);
     };
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-        const int e = 64 * j + (int)lane;
-        key[j] = x[j];
-        if (!by_logit && x[j] != NONE)
-            key[j] = score(x[j]) + (a.bias ? (double)a.bias[e] : 0.0);
-    }
     if (a.n_groups > 1) {
-        // Lane g keeps group g's score: the sum of its best group_topk keys.
-        const int per = E / a.n_groups;
-        double gs = NONE;
-        for (int g = 0; g < a.n_groups; g++) {
-            double sum = 0.0;
-            int first = -1;
-            for (int r = 0; r < a.group_topk; r++) {
-                double v = NONE;
-                int i = E;
+        // Lane g sums up groups g, g + L, ...: their best one or two keys.
 #pragma unroll
-                for (int j = 0; j < V; j++) {
-                    const int e = 64 * j + (int)lane;
-                    if (e / per == g && e < E && e != first)
-                        argmax_step(v, i, key[j], e);
+        for (int j = 0; j < V; j++)
+            lds[l * V + j] = key[j];
+        constexpr int GS = 64 / L;
+        T gs[GS];
+#pragma unroll
+        for (int i = 0; i < GS; i++) {
+            const int g = l + L * i;
+            T m1 = none<T>(), m2 = none<T>();
+            if (g < a.n_groups)
+                for (int k = 0; k < a.per_group; k++) {
+                    const T v = lds[g * a.per_group + k];
+                    const T lo = v > m1 ? m1 : v;
+                    m1 = v > m1 ? v : m1;
+                    m2 = lo > m2 ? lo : m2;
                 }
-                wave_argmax(v, i, lane);
-                if (v == NONE)
-                    break;
-                sum += v;
-                if (r == 0)
-                    first = i;
-            }
-            if ((int)lane == g)
-                gs = first < 0 ? NONE : sum;
+            gs[i] = a.group_topk == 2 && m2 != none<T>() ? m1 + m2 : m1;
         }
         uint64_t keep = 0;
-        for (int r = 0; r < a.topk_groups; r++) {
-            double v = gs;
-            int i = (int)lane;
-            wave_argmax(v, i, lane);
-            keep |= (uint64_t)1 << i;
-            if ((int)lane == i)
-                gs = NONE;
+        T last = none<T>();
+        for (int r = 0; r <= a.topk_groups; r++) {
+            T v = gs[0];
+#pragma unroll
+            for (int i = 1; i < GS; i++)
+                v = gs[i] > v ? gs[i] : v;
+            v = over_lanes<L>(v, MaxOf{});
+            if (r == a.topk_groups) {             // the best group left out
+                sure = sure && !close_keys(last, v);
+                break;
+            }
+            int g = 1 << 20;
+#pragma unroll
+            for (int i = GS - 1; i >= 0; i--)
+                g = gs[i] == v ? l + L * i : g;
+            g = over_lanes<L>(g, MinOf{});
+            if (v != none<T>())
+                keep |= (uint64_t)1 << g;
+#pragma unroll
+            for (int i = 0; i < GS; i++)
+                gs[i] = l + L * i == g ? none<T>() : gs[i];
+            last = v;
         }
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            const int e = 64 * j + (int)lane;
-            if (e < E && !((keep >> (e / per)) & 1))
-                key[j] = NONE;
+            const uint32_t e = (uint32_t)(l * V + j);
+            const uint32_t g = udiv(e, a.per_div);
+            key[j] = g < 64 && ((keep >> g) & 1) ? key[j] : none<T>();
         }
     }
-    // Lane c keeps the c-th choice.
-    double sel = 0.0;
-    int chosen = -1;
-    for (int c = 0; c < a.top_k; c++) {
-        double v = NONE;
-        int i = 64 * V;
-#pragma unroll
-        for (int j = 0; j < V; j++)
-            argmax_step(v, i, key[j], 64 * j + (int)lane);
-        wave_argmax(v, i, lane);
-        if (v == NONE)
+    *chosen = -1;
+    T last = none<T>();
+    for (int c = 0; c <= a.top_k; c++) {
+        if (c == a.top_k && by_logit)
             break;
-        double xv = 0.0;
+        int i;
+        const T v = best_key<L, V, T>(key, l, &i);
+        if (c > 0)
+            sure = sure && !close_keys(last, v);
+        if (c == a.top_k)
+            break;
+        const bool some = v != none<T>();
+        if (l == c)
+            *chosen = some ? i : -1;
 #pragma unroll
         for (int j = 0; j < V; j++)
-            if (64 * j + (int)lane == i) {
-                key[j] = NONE;
-                xv = x[j];
-            }
-        xv = lane_get(xv, (uint32_t)i & 63);
-        if ((int)lane == c) {
-            chosen = i;
-            sel = xv;
-        }
+            key[j] = l * V + j == i ? none<T>() : key[j];
+        last = v;
     }
-    // Renormalized weights depend on the scores' ratios alone: a softmax over
-    // the selected logits, or sigmoids scaled by e^-top where the largest
-    // selected logit, top, is negative, so that no sum underflows.
-    if (chosen >= 0 && !a.renorm)
-        sel = score(sel);
-    if (a.renorm) {
-        double top = chosen >= 0 ? sel : NONE;
-        int dummy = 0;
-        wave_argmax(top, dummy, lane);
-        if (a.sigmoid && top > 0.0)
-            top = 0.0;
-        if (chosen < 0)
-            sel = 0.0;
-        else if (!a.sigmoid)
-            sel = exp_f64(sel - top);
-        else
-            sel = sel >= 0.0 ? 1.0 / (1.0 + exp_f64(-sel))
-                             : exp_f64(sel - top) / (1.0 + exp_f64(sel));
-    }
-    if (a.renorm) {
-        const double s = wave_sum_f64(sel, lane);
-        sel = s > 0.0 ? sel / s : 0.0;
-    }
-    if ((int)lane < a.top_k) {
-        a.weights[t * a.top_k + lane] = (float)(sel * (double)a.scale);
-        a.experts[t * a.top_k + lane] = chosen;
-    }
+    return sure;
 }
 
-// Bit t of mask[e][w]: token 64 w + t of the tile chose expert e.  Bits are
-// set with LDS atomics (whose order cannot matter) and ranks are population
-// counts, so the maps do not depend on any order of execution.
-__device__ __forceinline__ void tile_masks(uint64_t *mask, const int64_t *experts, int64_t t0,
-                                           int tokens, int top_k, int E)
-{
-    for (int i = (int)tid(); i < E * MAP_WORDS; i += MAP_THREADS)
-        mask[i] = 0;
-    __syncthreads();
-    for (int i = (int)tid(); i < tokens * top_k; i += MAP_THREADS) {
-        const int64_t e = experts[t0 * top_k + i];
-        const int t = i / top_k;
-        if (e >= 0)
-            __hip_atomic_fetch_or(&mask[e * MAP_WORDS + (t >> 6)], (uint64_t)1 << (t & 63),
-                                  __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-    }
-    __syncthreads();
-}
 __device__ __forceinline__ int popc(uint64_t v) { return __builtin_popcountll(v); }
 
-__global__ void __launch_bounds__(MAP_THREADS) moe_count_kernel(const int64_t *experts,
-                                                                int64_t n_tokens, int top_k,
-                                                                int E, int *hist)
+// Inclusive sum over the 64 lanes.
+__device__ __forceinline__ int wave_scan(int v)
 {
-    extern __shared__ uint64_t mask[];
-    const int64_t t0 = (int64_t)wg_id() * MAP_TOKENS;
-    const int tokens = (int)(n_tokens - t0 < MAP_TOKENS ? n_tokens - t0 : MAP_TOKENS);
-    tile_masks(mask, experts, t0, tokens, top_k, E);
-    for (int e = (int)tid(); e < E; e += MAP_THREADS) {
-        int n = 0;
+    const int lane = (int)lane_id();
 #pragma unroll
-        for (int w = 0; w < MAP_WORDS; w++)
-            n += popc(mask[e * MAP_WORDS + w]);
-        hist[(int64_t)wg_id() * E + e] = n;
+    for (int k = 1; k < 64; k <<= 1) {
+        const int o = lane_get(v, (uint32_t)(lane >= k ? lane - k : lane));
+        v += lane >= k ? o : 0;
+    }
+    return v;
+}
+// base[e] = sum of n[0 .. e) for e <= E, by the first wavefront of a workgroup.
+__device__ __forceinline__ void expert_bases(int *base, const int *n, int E)
+{
+    if (wave_in_group() == 0) {
+        int carry = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int e = e0 + (int)lane_id();
+            const int v = e < E ? n[e] : 0, s = wave_scan(v);
+            if (e < E)
+                base[e] = carry + s - v;
+            carry += __builtin_amdgcn_readlane(s, 63);
+        }
+        if (lane_id() == 0)
+            base[E] = carry;
     }
 }
-
-// Tile w's copies to their rows: the first row of expert e (the counts of
-// the experts before it), the copies of earlier tiles, the earlier tokens
-// of the tile.
-__global__ void __launch_bounds__(MAP_THREADS) moe_maps_kernel(
-    const int64_t *experts, int64_t n_tokens, int top_k, int E, int n_tiles, const int *hist,
-    int64_t *token_rows, int64_t *row_tokens, int64_t *seg_offsets)
+// The copies of tile t0 .. to their rows: the first row of (tile, expert) and
+// the tokens of the tile before.
+__device__ __forceinline__ void write_rows(const uint64_t *mask, const int *first,
+                                           const int64_t *experts, int64_t t0, int tokens,
+                                           int top_k, int64_t *token_rows, int64_t *row_tokens)
 {
-    extern __shared__ uint64_t mask[];
-    int *base = reinterpret_cast<int *>(mask + E * MAP_WORDS);      // [E + 1]
-    int *before = base + E + 1;                                     // [E]
-    const int tile = (int)wg_id();
-    const int64_t t0 = (int64_t)tile * MAP_TOKENS;
-    const int tokens = (int)(n_tokens - t0 < MAP_TOKENS ? n_tokens - t0 : MAP_TOKENS);
-    for (int e = (int)tid(); e < E; e += MAP_THREADS) {
-        int n = 0, b = 0;
-        for (int i = 0; i < n_tiles; i++) {
-            if (i == tile)
-                b = n;
-            n += hist[(int64_t)i * E + e];
-        }
-        base[e + 1] = n;
-        before[e] = b;
-    }
-    tile_masks(mask, experts, t0, tokens, top_k, E);
-    if (tid() == 0) {
-        int n = 0;
-        base[0] = 0;
-        for (int e = 0; e < E; e++) {
-            n += base[e + 1];
-            base[e + 1] = n;
-        }
-    }
-    __syncthreads();
-    for (int i = (int)tid(); i < tokens * top_k; i += MAP_THREADS) {
-        const int64_t g = t0 * top_k + i;
-        const int64_t e = experts[g];
-        const int t = i / top_k;
+    for (int i = (int)tid(); i < tokens * top_k; i += ROUTE_THREADS) {
+        const int64_t g = t0 * top_k + i, e = experts[g];
+        const int t = (int)((uint32_t)i / (uint32_t)top_k);
         int64_t row = -1;
         if (e >= 0) {
-            int r = base[e] + before[e];
-            for (int w = 0; w < (t >> 6); w++)
-                r += popc(mask[e * MAP_WORDS + w]);
-            r += popc(mask[e * MAP_WORDS + (t >> 6)] & (((uint64_t)1 << (t & 63)) - 1));
-            row = r;
+            row = first[e] + popc(mask[e] & (((uint64_t)1 << t) - 1));
             row_tokens[row] = t0 + t;
         }
         token_rows[g] = row;
     }
-    // Dropped copies leave rows past the last segment; their token is -1.
-    const int64_t total = n_tokens * top_k;
-    for (int64_t r = base[E] + (int64_t)tile * MAP_THREADS + tid(); r < total;
-         r += (int64_t)n_tiles * MAP_THREADS)
+}
+// Dropped copies leave rows past the last segment; their token is -1.
+__device__ __forceinline__ void write_tail(int64_t used, int64_t total, int wg, int wgs,
+                                           int64_t *row_tokens)
+{
+    for (int64_t r = used + (int64_t)wg * ROUTE_THREADS + tid(); r < total;
+         r += (int64_t)wgs * ROUTE_THREADS)
         row_tokens[r] = -1;
+}
+
+template <bool BF16, int L, int V>
+__global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(RouteArgs a)
+{
+    constexpr int SLOTS = ROUTE_THREADS / L;      // tokens at once
+    extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
+    // Keys of every slot's token (groups), then the tile's masks and first rows (maps).
+    double *keys = reinterpret_cast<double *>(shared);
+    uint64_t *mask = reinterpret_cast<uint64_t *>(shared + (a.n_groups > 1 ? SLOTS * L * V * 8 : 0));
+    const int E = a.n_experts, l = (int)tid() % L, slot = (int)tid() / L;
+    const int64_t t0 = (int64_t)wg_id() * MAP_TOKENS;
+    const int tokens = (int)(a.n_tokens - t0 < MAP_TOKENS ? a.n_tokens - t0 : MAP_TOKENS);
+    if (a.masks) {
+        for (int e = (int)tid(); e < E; e += ROUTE_THREADS)
+            mask[e] = 0;
+        __syncthreads();
+    }
+    for (int i = 0; i < tokens; i += SLOTS) {
+        // Slots past the last token repeat it and write nothing.
+        const int i0 = i + slot < tokens ? i + slot : tokens - 1;
+        const int64_t t = t0 + i0;
+        const bool live = i + slot < tokens;
+        float x[V], bias[V];
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            const int e = l * V + j;
+            float f = -__builtin_inff();
+            bias[j] = 0.0f;
+            if (e < E) {
+                f = ld_elem<BF16>(a.logits, t * E + e);
+                bool out = is_masked(f);
+                if (a.bias) {
+                    bias[j] = a.bias[e];
+                    out = out || is_masked(bias[j]);
+                }
+                f = out ? -__builtin_inff() : f;
+                f = f < 3.402823466e+38f ? f : 3.402823466e+38f;
+            }
+            x[j] = f;
+        }
+        int chosen;
+        float top, den;
+        bool sure = choose<L, V, float>(a, x, bias, l, reinterpret_cast<float *>(keys + slot * L * V),
+                                        &chosen, &top, &den);
+        if (__builtin_amdgcn_ballot_w64(!sure) != 0) {
+            double top64, den64;
+            (void)choose<L, V, double>(a, x, bias, l, keys + slot * L * V, &chosen, &top64, &den64);
+        }
+        // Weights.  Renormalized ones depend on the scores' ratios alone: a softmax over
+        // the selected logits, or sigmoids scaled by e^-top where the largest selected
+        // logit, top, is negative, so that no sum underflows.
+        const bool mine = l < a.top_k && chosen >= 0;
+        float xv = mine ? ld_elem<BF16>(a.logits, t * E + chosen) : -__builtin_inff();
+        xv = xv < 3.402823466e+38f ? xv : 3.402823466e+38f;
+        float w = 0.0f;
+        if (a.renorm) {
+            float h = over_lanes<L>(xv, MaxOf{});
+            h = a.sigmoid && h > 0.0f ? 0.0f : h;
+            if (mine)
+                w = !a.sigmoid ? exp_f32(xv - h)
+                    : xv >= 0.0f ? 1.0f / (1.0f + exp_f32(-xv))
+                                 : exp_f32(xv - h) / (1.0f + exp_f32(xv));
+            const float s = over_lanes<L>(w, SumOf{});
+            w = s > 0.0f ? w / s : 0.0f;
+        } else if (mine) {
+            w = a.sigmoid ? 1.0f / (1.0f + exp_f32(-xv)) : exp_f32(xv - top) / den;
+        }
+        if (live && l < a.top_k) {
+            a.weights[t * a.top_k + l] = w * a.scale;
+            a.experts[t * a.top_k + l] = chosen;
+            if (a.masks && chosen >= 0)
+                __hip_atomic_fetch_or(&mask[chosen], (uint64_t)1 << i0, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+    }
+    if (!a.masks)
+        return;
+    __syncthreads();
+    if (a.token_rows) {                           // the only tile
+        int *base = reinterpret_cast<int *>(mask + E), *n = base + E + 1;
+        for (int e = (int)tid(); e < E; e += ROUTE_THREADS)
+            n[e] = popc(mask[e]);
+        __syncthreads();
+        expert_bases(base, n, E);
+        __syncthreads();
+        write_rows(mask, base, a.experts, t0, tokens, a.top_k, a.token_rows, a.row_tokens);
+        write_tail(base[E], (int64_t)tokens * a.top_k, 0, 1, a.row_tokens);
+        for (int e = (int)tid(); e <= E; e += ROUTE_THREADS)
+            a.seg_offsets[e] = base[e];
+        return;
+    }
+    for (int e = (int)tid(); e < E; e += ROUTE_THREADS)
+        a.masks[(int64_t)wg_id() * E + e] = mask[e];
+}
+
+// One wavefront per expert: before[tile][e] = its copies in earlier tiles,
+// total[e] all of them.
+__global__ void __launch_bounds__(64) moe_sum_kernel(const uint64_t *masks, int E, int n_tiles,
+                                                     int *before, int *total)
+{
+    const int e = (int)wg_id(), lane = (int)lane_id();
+    int carry = 0;
+    for (int i0 = 0; i0 < n_tiles; i0 += 64) {
+        const int i = i0 + lane;
+        const int v = i < n_tiles ? popc(masks[(int64_t)i * E + e]) : 0, s = wave_scan(v);
+        if (i < n_tiles)
+            before[(int64_t)i * E + e] = carry + s - v;
+        carry += __builtin_amdgcn_readlane(s, 63);
+    }
+    if (lane == 0)
+        total[e] = carry;
+}
+
+// One tile a workgroup.  total == nullptr: the sums over tiles are formed here.
+__global__ void __launch_bounds__(ROUTE_THREADS) moe_maps_kernel(
+    const int64_t *experts, int64_t n_tokens, int top_k, int E, int n_tiles,
+    const uint64_t *masks, const int *before, const int *total, int64_t *token_rows,
+    int64_t *row_tokens, int64_t *seg_offsets)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
+    uint64_t *mask = reinterpret_cast<uint64_t *>(shared);          // [E]
+    int *n = reinterpret_cast<int *>(mask + E), *base = n + E;       // [E], [E + 1]
+    int *first = base + E + 1;                                       // [E]
+    const int tile = (int)wg_id();
+    const int64_t t0 = (int64_t)tile * MAP_TOKENS;
+    const int tokens = (int)(n_tokens - t0 < MAP_TOKENS ? n_tokens - t0 : MAP_TOKENS);
+    for (int e = (int)tid(); e < E; e += ROUTE_THREADS) {
+        mask[e] = masks[(int64_t)tile * E + e];
+        if (total) {
+            n[e] = total[e];
+            first[e] = before[(int64_t)tile * E + e];
+        } else {
+            int all = 0, b = 0;
+            for (int i = 0; i < n_tiles; i++) {
+                b = i == tile ? all : b;
+                all += popc(masks[(int64_t)i * E + e]);
+            }
+            n[e] = all;
+            first[e] = b;
+        }
+    }
+    __syncthreads();
+    expert_bases(base, n, E);
+    __syncthreads();
+    for (int e = (int)tid(); e < E; e += ROUTE_THREADS)
+        first[e] += base[e];
+    __syncthreads();
+    write_rows(mask, first, experts, t0, tokens, top_k, token_rows, row_tokens);
+    write_tail(base[E], n_tokens * top_k, tile, n_tiles, row_tokens);
     if (tile == 0)
-        for (int e = (int)tid(); e <= E; e += MAP_THREADS)
+        for (int e = (int)tid(); e <= E; e += ROUTE_THREADS)
             seg_offsets[e] = base[e];
 }
 
@@ -293,27 +443,37 @@ __global__ void __launch_bounds__(MAP_THREADS) moe_maps_kernel(
 
 static int64_t map_tiles(int64_t n_tokens) { return (n_tokens + MAP_TOKENS - 1) / MAP_TOKENS; }
 
+// Masks, sums before a tile, totals.
 int64_t moe_route_workspace(int64_t n_tokens, int64_t n_experts)
 {
-    return map_tiles(n_tokens) * n_experts * (int64_t)sizeof(int);
+    return (map_tiles(n_tokens) * (8 + 4) + 4) * n_experts;
 }
 
+// L lanes a token and V experts a lane.
 template <bool BF16>
 static void route_launch(const RouteArgs &a, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((a.n_tokens + ROUTE_WAVES - 1) / ROUTE_WAVES)),
-        block(64 * ROUTE_WAVES);
-    const int v = (a.n_experts + 63) / 64;
-    if (v <= 1)
-        hipLaunchKernelGGL((moe_route_kernel<BF16, 1>), grid, block, 0, stream, a);
-    else if (v <= 2)
-        hipLaunchKernelGGL((moe_route_kernel<BF16, 2>), grid, block, 0, stream, a);
-    else if (v <= 4)
-        hipLaunchKernelGGL((moe_route_kernel<BF16, 4>), grid, block, 0, stream, a);
-    else if (v <= 8)
-        hipLaunchKernelGGL((moe_route_kernel<BF16, 8>), grid, block, 0, stream, a);
+    const dim3 grid((unsigned)map_tiles(a.n_tokens)), block(ROUTE_THREADS);
+    const bool narrow = a.n_experts <= 256 && a.top_k <= 16;
+    const int lanes = narrow ? 16 : 64, v = (a.n_experts + lanes - 1) / lanes;
+    int vp = 1;
+    while (vp < v)
+        vp *= 2;
+    const size_t lds = (a.n_groups > 1 ? (size_t)ROUTE_THREADS * vp * 8 : 0) +
+                       (a.masks ? (size_t)a.n_experts * 16 + 8 : 0);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, stream, a); };
+    if (narrow)
+        vp == 1   ? go(moe_route_kernel<BF16, 16, 1>)
+        : vp == 2 ? go(moe_route_kernel<BF16, 16, 2>)
+        : vp == 4 ? go(moe_route_kernel<BF16, 16, 4>)
+        : vp == 8 ? go(moe_route_kernel<BF16, 16, 8>)
+                  : go(moe_route_kernel<BF16, 16, 16>);
     else
-        hipLaunchKernelGGL((moe_route_kernel<BF16, 16>), grid, block, 0, stream, a);
+        vp == 1   ? go(moe_route_kernel<BF16, 64, 1>)
+        : vp == 2 ? go(moe_route_kernel<BF16, 64, 2>)
+        : vp == 4 ? go(moe_route_kernel<BF16, 64, 4>)
+        : vp == 8 ? go(moe_route_kernel<BF16, 64, 8>)
+                  : go(moe_route_kernel<BF16, 64, 16>);
 }
 
 hipError_t launch_moe_route(bool bf16, const void *logits, const float *bias, int64_t n_tokens,
@@ -321,35 +481,44 @@ hipError_t launch_moe_route(bool bf16, const void *logits, const float *bias, in
                             int64_t *experts, int64_t *token_rows, int64_t *row_tokens,
                             int64_t *seg_offsets, void *workspace, hipStream_t stream)
 {
-    RouteArgs a{logits, bias, n_tokens, (int)n_experts, (int)p.top_k, (int)p.n_groups,
-                (int)p.topk_groups, (int)p.group_topk, p.scoring == MXQ_SCORE_SIGMOID,
-                p.renormalize != 0, p.scale, weights, experts};
+    const int E = (int)n_experts, tiles = (int)map_tiles(n_tokens);
+    const bool one = tiles == 1;
+    uint64_t *masks = token_rows ? static_cast<uint64_t *>(workspace) : nullptr;
+    const int per = E / (int)p.n_groups;
+    const RouteArgs a{logits, bias, n_tokens, E, (int)p.top_k, (int)p.n_groups,
+                      (int)p.topk_groups, (int)p.group_topk, per, make_div((uint32_t)per),
+                      p.scoring == MXQ_SCORE_SIGMOID, p.renormalize != 0, p.scale, weights,
+                      experts, one ? token_rows : nullptr, row_tokens, seg_offsets, masks};
     if (bf16)
         route_launch<true>(a, stream);
     else
         route_launch<false>(a, stream);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !token_rows)
+    if (e != hipSuccess || !token_rows || one)
         return e;
-    const int E = (int)n_experts, tiles = (int)map_tiles(n_tokens);
-    const size_t mask_bytes = (size_t)E * MAP_WORDS * 8;
-    hipLaunchKernelGGL(moe_count_kernel, dim3(tiles), dim3(MAP_THREADS), mask_bytes, stream,
-                       experts, n_tokens, (int)p.top_k, E, static_cast<int *>(workspace));
-    e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    hipLaunchKernelGGL(moe_maps_kernel, dim3(tiles), dim3(MAP_THREADS),
-                       mask_bytes + (2 * (size_t)E + 1) * 4, stream, experts, n_tokens,
-                       (int)p.top_k, E, tiles, static_cast<const int *>(workspace), token_rows,
-                       row_tokens, seg_offsets);
+    int *before = reinterpret_cast<int *>(masks + (int64_t)tiles * E);
+    int *total = before + (int64_t)tiles * E;
+    const bool sums = tiles > MAP_SELF_TILES;
+    if (sums) {
+        hipLaunchKernelGGL(moe_sum_kernel, dim3(E), dim3(64), 0, stream, masks, E, tiles, before,
+                           total);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL(moe_maps_kernel, dim3(tiles), dim3(ROUTE_THREADS), (size_t)E * 20 + 4,
+                       stream, experts, n_tokens, (int)p.top_k, E, tiles, masks, before,
+                       sums ? total : nullptr, token_rows, row_tokens, seg_offsets);
     return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // Router gradient.  With s the scores, S the sum of the selected ones and
-// g_i = scale dw_i: renormalized ds_i = (g_i - sum_j g_j s_j / S) / S,
-// otherwise ds_i = g_i; then dx_e = s_e (1 - s_e) ds_e (sigmoid) or
-// s_e (ds_e - sum_j ds_j s_j) (softmax), ds_e = 0 for unselected experts.
+// g_i = scale dw_i: renormalized ds_i = sum_j (g_i - g_j) s_j / S^2 (the form
+// in which equal g_i, and a single choice, give exactly 0), otherwise ds_i =
+// g_i; then dx_e = s_e (1 - s_e) ds_e (sigmoid) or s_e (ds_e - sum_j ds_j
+// s_j) (softmax; the sum is 0 for renormalized weights), ds_e = 0 for
+// unselected experts.  One read of the logits, one write of the gradient.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -364,87 +533,80 @@ struct RouteBwdArgs {
     void *d_logits;
 };
 
-template <bool BF16, int V>
-__global__ void __launch_bounds__(64 * ROUTE_WAVES) moe_route_backward_kernel(RouteBwdArgs a)
+// L lanes a token; lane l holds experts l, l + L, ... (coalesced), and choice l.
+template <bool BF16, int L, int V>
+__global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(RouteBwdArgs a)
 {
-    const uint32_t lane = lane_id();
-    const int64_t t = (int64_t)wg_id() * ROUTE_WAVES + wave_in_group();
-    if (t >= a.n_tokens)
-        return;
+    const int l = (int)tid() % L;
+    const int64_t t = (int64_t)wg_id() * (ROUTE_THREADS / L) + tid() / L;
+    const bool live = t < a.n_tokens;
+    const int64_t tt = live ? t : a.n_tokens - 1;
     const int E = a.n_experts;
-    float s[V], ds[V];
+    constexpr float LOW = -3.402823466e+38f;
+    auto score_in = [&](float f) { return f < -LOW ? f : -LOW; };
+    float s[V], m = LOW;
     bool dead[V];
-    float m = -3.402823466e+38f;
 #pragma unroll
     for (int j = 0; j < V; j++) {
-        const int e = 64 * j + (int)lane;
-        float f = e < E ? ld_elem<BF16>(a.logits, t * E + e) : -__builtin_inff();
+        const int e = L * j + l;
+        const float f = e < E ? ld_elem<BF16>(a.logits, tt * E + e) : -__builtin_inff();
         dead[j] = is_masked(f);
-        f = f < 3.402823466e+38f ? f : 3.402823466e+38f;
-        s[j] = dead[j] ? -3.402823466e+38f : f;
+        s[j] = dead[j] ? LOW : score_in(f);
         m = s[j] > m ? s[j] : m;
-        ds[j] = 0.0f;
     }
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-        const float o = lane_get(m, lane ^ k);
-        m = o > m ? o : m;
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-        if (a.sigmoid)
-            s[j] = dead[j] ? 0.0f : 1.0f / (1.0f + exp_f32(-s[j]));
-        else
-            s[j] = dead[j] ? 0.0f : exp_f32(s[j] - m);
-        sum += s[j];
-    }
+    // Choice l of the token: its expert, gradient and logit.
+    int64_t e64 = l < a.top_k ? a.experts[tt * a.top_k + l] : -1;
+    const int ce = e64 >= 0 && e64 < E ? (int)e64 : -1;
+    const float cg = ce >= 0 ? a.d_weights[tt * a.top_k + l] * a.scale : 0.0f;
+    float cx = ce >= 0 ? ld_elem<BF16>(a.logits, tt * E + ce) : -__builtin_inff();
+    const bool cdead = is_masked(cx);
+    cx = cdead ? LOW : score_in(cx);
+    float r = 1.0f;
     if (!a.sigmoid) {
-        sum = wave_sum_f32(sum);
-        const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+        m = over_lanes<L>(m, MaxOf{});
+        float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; j++)
-            s[j] *= r;
-    }
-    float S = 0.0f, gs = 0.0f;
-    for (int c = 0; c < a.top_k; c++) {
-        const int64_t e64 = a.experts[t * a.top_k + c];
-        if (e64 < 0 || e64 >= E)
-            continue;
-        const int e = (int)e64;
-        const float g = a.d_weights[t * a.top_k + c] * a.scale;
-#pragma unroll
-        for (int j = 0; j < V; j++)
-            if (64 * j + (int)lane == e) {
-                ds[j] += g;
-                S += s[j];
-                gs += g * s[j];
-            }
-    }
-    S = wave_sum_f32(S);
-    gs = wave_sum_f32(gs);
-    if (a.renorm) {
-        const float r = S > 0.0f ? 1.0f / S : 0.0f;
-        const float mean = gs * r;
-        for (int c = 0; c < a.top_k; c++) {
-            const int64_t e64 = a.experts[t * a.top_k + c];
-            if (e64 < 0 || e64 >= E)
-                continue;
-#pragma unroll
-            for (int j = 0; j < V; j++)
-                if (64 * j + (int)lane == (int)e64)
-                    ds[j] -= mean;
+        for (int j = 0; j < V; j++) {
+            s[j] = dead[j] ? 0.0f : exp_f32(s[j] - m);
+            sum += s[j];
         }
+        sum = over_lanes<L>(sum, SumOf{});
+        r = sum > 0.0f ? 1.0f / sum : 0.0f;
+    }
+    auto sigmoid = [](float v) { return 1.0f / (1.0f + exp_f32(-v)); };
+#pragma unroll
+    for (int j = 0; j < V; j++)
+        s[j] = a.sigmoid ? (dead[j] ? 0.0f : sigmoid(s[j])) : s[j] * r;
+    const float cs = cdead ? 0.0f : a.sigmoid ? sigmoid(cx) : exp_f32(cx - m) * r;
+    // ds of every choice, then to the experts' lanes.
+    const uint32_t lane0 = lane_id() & ~(uint32_t)(L - 1);
+    float S = 0.0f, cd = cg, gs = 0.0f;
+    if (a.renorm) {
+        cd = 0.0f;
+        for (int c = 0; c < a.top_k; c++) {
+            const float sc = lane_get(cs, lane0 + c), gc = lane_get(cg, lane0 + c);
+            S += sc;
+            cd = __builtin_fmaf(cg - gc, sc, cd);
+        }
+        const float q = S > 0.0f ? 1.0f / S : 0.0f;
+        cd = ce >= 0 ? cd * q * q : 0.0f;
+    } else if (!a.sigmoid) {
+        for (int c = 0; c < a.top_k; c++)
+            gs = __builtin_fmaf(lane_get(cg, lane0 + c), lane_get(cs, lane0 + c), gs);
+    }
+    float ds[V] = {};
+    for (int c = 0; c < a.top_k; c++) {
+        const int ec = lane_get(ce, lane0 + c);
+        const float dc = lane_get(cd, lane0 + c);
 #pragma unroll
         for (int j = 0; j < V; j++)
-            ds[j] *= r;
-        gs = 0.0f;      // sum_j ds_j s_j of renormalized weights
+            ds[j] += L * j + l == ec ? dc : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < V; j++) {
-        const int e = 64 * j + (int)lane;
+        const int e = L * j + l;
         const float d = a.sigmoid ? ds[j] * s[j] * (1.0f - s[j]) : s[j] * (ds[j] - gs);
-        if (e < E)
+        if (live && e < E)
             st_elem<BF16>(a.d_logits, t * E + e, d);
     }
 }
@@ -452,19 +614,21 @@ __global__ void __launch_bounds__(64 * ROUTE_WAVES) moe_route_backward_kernel(Ro
 template <bool BF16>
 void route_backward_launch(const RouteBwdArgs &a, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((a.n_tokens + ROUTE_WAVES - 1) / ROUTE_WAVES)),
-        block(64 * ROUTE_WAVES);
-    const int v = (a.n_experts + 63) / 64;
-    if (v <= 1)
-        hipLaunchKernelGGL((moe_route_backward_kernel<BF16, 1>), grid, block, 0, stream, a);
-    else if (v <= 2)
-        hipLaunchKernelGGL((moe_route_backward_kernel<BF16, 2>), grid, block, 0, stream, a);
-    else if (v <= 4)
-        hipLaunchKernelGGL((moe_route_backward_kernel<BF16, 4>), grid, block, 0, stream, a);
-    else if (v <= 8)
-        hipLaunchKernelGGL((moe_route_backward_kernel<BF16, 8>), grid, block, 0, stream, a);
+    const bool narrow = a.n_experts <= 256 && a.top_k <= 16;
+    const int lanes = narrow ? 16 : 64, v = (a.n_experts + lanes - 1) / lanes;
+    const int slots = ROUTE_THREADS / lanes;
+    const dim3 grid((unsigned)((a.n_tokens + slots - 1) / slots)), block(ROUTE_THREADS);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+    if (narrow)
+        v <= 2    ? go(moe_route_backward_kernel<BF16, 16, 2>)
+        : v <= 4  ? go(moe_route_backward_kernel<BF16, 16, 4>)
+        : v <= 8  ? go(moe_route_backward_kernel<BF16, 16, 8>)
+        : v <= 12 ? go(moe_route_backward_kernel<BF16, 16, 12>)
+                  : go(moe_route_backward_kernel<BF16, 16, 16>);
     else
-        hipLaunchKernelGGL((moe_route_backward_kernel<BF16, 16>), grid, block, 0, stream, a);
+        v <= 2   ? go(moe_route_backward_kernel<BF16, 64, 2>)
+        : v <= 8 ? go(moe_route_backward_kernel<BF16, 64, 8>)
+                 : go(moe_route_backward_kernel<BF16, 64, 16>);
 }
 
 }  // namespace
