@@ -19,7 +19,7 @@ def _bf16_bits(x: torch.Tensor) -> torch.Tensor:
 
 
 def _empty(shape, dtype, like):
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    return like.new_empty(shape, dtype=dtype)
 
 
 class MXFP8RowCol(NamedTuple):
@@ -402,13 +402,21 @@ def _out_code(dtype) -> int:
     return B.MXQ_OUT_BF16 if dtype == torch.bfloat16 else B.MXQ_OUT_F32
 
 
-def _arg(t, what: str, dtype, shape=None):
-    """A tensor argument of the given dtype and shape (None: any size), contiguous."""
+def _arg(t, what: str, dtype, shape):
+    """A tensor argument of the given dtype and shape (None: any size), contiguous.
+    A small call checks up to twenty of these while its kernel takes a few
+    microseconds, so an argument that fits takes three comparisons."""
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or
-                              any(w is not None and n != w for n, w in zip(t.shape, shape))):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    s = t.shape
+    if s != shape:
+        fits = len(s) == len(shape)
+        if fits:
+            for n, w in zip(s, shape):
+                if n != w and w is not None:
+                    fits = False
+        if not fits:
+            raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(s)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t
@@ -626,10 +634,11 @@ def nvfp4_attention(q, k: NVFP4, v: NVFP4, block_table, seq_lens, n_kv_heads: in
     _arg(q, "q", torch.bfloat16, (None, None, None, None))
     n_seqs, q_len, n_heads, D = q.shape
     n_rows = _arg(k.codes, "k codes", torch.uint8, (None, D // 2)).shape[0]
-    for name, c in (("k", k), ("v", v)):
-        _arg(c.codes, f"{name} codes", torch.uint8, (n_rows, D // 2))
-        _arg(c.block_scales, f"{name} block scales", torch.uint8, (n_rows, D // 16))
-        _arg(c.fp32_scales, f"{name} FP32 scales", torch.float32, (n_rows,))
+    _arg(v.codes, "v codes", torch.uint8, (n_rows, D // 2))
+    _arg(k.block_scales, "k block scales", torch.uint8, (n_rows, D // 16))
+    _arg(v.block_scales, "v block scales", torch.uint8, (n_rows, D // 16))
+    _arg(k.fp32_scales, "k FP32 scales", torch.float32, (n_rows,))
+    _arg(v.fp32_scales, "v FP32 scales", torch.float32, (n_rows,))
     max_pages = _arg(block_table, "block_table", torch.int64, (n_seqs, None)).shape[1]
     _arg(seq_lens, "seq_lens", torch.int64, (n_seqs,))
     per_page = n_kv_heads * page_size
