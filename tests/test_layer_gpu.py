@@ -776,3 +776,95 @@ def test_api_refuses_wrong_arguments():
         api.nvfp4_attention(q, cache, cache, table, lens, 2, 16, causal=False, window=4)
     with pytest.raises(TypeError):
         api.nvfp4_attention(q.float(), cache, cache, table, lens, 2, 16)
+
+
+# ---------------------------------------------------------------------------
+# The operators together
+# ---------------------------------------------------------------------------
+
+def nvfp4_f64(w):
+    return R.decode(host(w.codes), host(w.block_scales)) * host(w.fp32_scales)[:, None].astype(
+        np.float64)
+
+
+def test_decode_block_in_a_graph():
+    """Steps of the example's block replayed from a graph give the bytes of the
+    eager steps of a second block, and each operator's output follows from
+    what the step handed to it."""
+    from examples.moe_block import DecodeBlock, Shape
+    s = Shape(hidden=256, inter=128, experts=12, top_k=3, heads=8, kv_heads=2, head_dim=64, page=16)
+    n, context = 3, 30
+    announce("decode block")
+    eager, block = (DecodeBlock(s, n, context, 48, seed=3) for _ in range(2))
+    rng = np.random.default_rng(43)
+    xs = [put(bf16(rng.normal(0, 1, (n, s.hidden))), torch.bfloat16) for _ in range(5)]
+    x = xs[0].clone()
+    block.step(x)
+    eager.step(xs[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, parts = block.step(x)
+    for xi in xs[1:]:
+        x.copy_(xi)
+        graph.replay()
+        want, other = eager.step(xi)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(parts["att"], other["att"])
+        assert torch.equal(parts["rows"], other["rows"])
+    assert block.lens.tolist() == [context + 5] * n
+
+    kk, vv = (nvfp4_f64(c) for c in block.cache)
+    q = parts["q"].cpu().double().numpy()[:, None]
+    sc = float(np.float32(s.head_dim ** -0.5))
+    want, _, mag, terms = R.attention(q, kk, vv, host(block.table), host(block.lens), s.kv_heads,
+                                      s.page, sc, True, 0)
+    delta = terms * (s.head_dim + 24) * 2.0 ** -23 + 2.0 ** -20
+    tol = mag * (R.HALF_FP16 + 2 * delta[..., None] + (35 / 16 + 64) * 2.0 ** -23)
+    close(parts["att"], want, tol + np.abs(want) * R.HALF_BF16 * 1.001, "attention of the step")
+    h2 = parts["h2"].cpu().double().numpy()
+    w = block.w_router
+    want, tol = product(h2, np.ones(n), R.decode(host(w.codes), host(w.block_scales)),
+                        np.repeat(host(w.fp32_scales), s.experts).astype(np.float64), 0.0)
+    close(parts["logits"], want, tol, "router logits of the step")
+    r = parts["routing"]
+    _, experts, *_ = R.route(parts["logits"].cpu().double().numpy(), None, params(s.top_k))
+    assert np.array_equal(host(r.experts), experts)
+    y = api.nvfp4_expert_layer(parts["h2"], r, block.gateup, block.down)
+    torch.cuda.synchronize()
+    assert torch.equal(y, parts["y"])
+
+
+def test_train_step():
+    """Values that MXFP8 holds exactly: every product of the step is exact, so
+    what is left is the BF16 rounding of each result."""
+    from examples.moe_block import train_step
+    rng = np.random.default_rng(47)
+    T, E, K, N, k = 50, 6, 256, 128, 2
+    announce("train step")
+    x, w, g = (rng.integers(-2, 3, shape).astype(np.float64)
+               for shape in ((T, K), (E, N, K), (T, N)))
+    z = rng.uniform(-3, 0, (T, E)).astype(np.float32).astype(np.float64)
+    pick = np.sort(np.argsort(rng.random((T, E)), 1)[:, :k], 1)
+    np.put_along_axis(z, pick, 1.0, 1)                       # two equal experts: weights of 1/2
+    s = train_step(put(x, torch.bfloat16), put(z, torch.float32), put(w, torch.bfloat16),
+                   put(g, torch.bfloat16), k)
+    torch.cuda.synchronize()
+    y = bf16(np.einsum("tk,tcnk->tcn", x, w[pick]))
+    want = 0.5 * y.sum(1)
+    tiny = 2.0 ** -20 * np.abs(y).sum(1)
+    close(s.out, want, tiny + np.abs(want) * R.HALF_BF16, "out")
+    dx = bf16(np.einsum("tn,tcnk->tck", 0.5 * g, w[pick]))
+    close(s.d_tokens, dx.sum(1), np.abs(dx.sum(1)) * R.HALF_BF16 + 2.0 ** -20 * np.abs(dx).sum(1),
+          "d_tokens")
+    de = np.zeros((E, N, K))
+    for t in range(T):
+        for e in pick[t]:
+            de[e] += np.outer(0.5 * g[t], x[t])
+    close(s.d_experts, de, np.zeros(de.shape), "d_experts")
+    dw = np.einsum("tn,tcn->tc", g, y)
+    # The two weights' fp32 sums, then the router's gradient: test_route_backward's bound.
+    dmag = np.einsum("tn,tcn->tc", np.abs(g), np.abs(y))
+    want, _ = R.route_backward(dw, z, pick, SOFTMAX, True, 1.0)
+    _, mag = R.route_backward(dmag, z, pick, SOFTMAX, True, 1.0)
+    close(s.d_logits, want, mag * (2.0 ** -19 + (90 + N) * 2.0 ** -24) + 1e-37, "d_logits")
