@@ -721,7 +721,7 @@ constexpr int COMBINE_THREADS = 256;              // at most; a thread takes 8 c
 constexpr int COMBINE_ROWS = 8;                   // rows of a token in flight
 
 // Eight values of a row (16 bytes of BF16, 32 of FP32), as loaded.  Rows are
-// read once: loads that do not stay in the caches.
+// read once and written once: accesses that do not stay in the caches.
 template <bool BF16>
 struct Raw8 {
     uint4 q[BF16 ? 1 : 2];
@@ -755,21 +755,24 @@ __device__ __forceinline__ void st8v(void *p, int64_t i, const float (&v)[8])
 #pragma unroll
         for (int k = 0; k < 4; k++)
             q[k] = (uint32_t)bf16_rne(v[2 * k]) | (uint32_t)bf16_rne(v[2 * k + 1]) << 16;
-        *reinterpret_cast<u32x4_t *>(reinterpret_cast<uint16_t *>(p) + i) = q;
+        __builtin_nontemporal_store(
+            q, reinterpret_cast<u32x4_t *>(reinterpret_cast<uint16_t *>(p) + i));
     } else {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             const u32x4_t q = {f2u(v[4 * h]), f2u(v[4 * h + 1]), f2u(v[4 * h + 2]),
                                f2u(v[4 * h + 3])};
-            *reinterpret_cast<u32x4_t *>(reinterpret_cast<float *>(p) + i + 4 * h) = q;
+            __builtin_nontemporal_store(
+                q, reinterpret_cast<u32x4_t *>(reinterpret_cast<float *>(p) + i + 4 * h));
         }
     }
 }
 
 // A workgroup per token (of as many threads as the columns want).  Bound by HBM:
-// 32768 tokens x 8 rows of 2048 BF16 take 213 us (1.21 GB, 5.7 TB/s).  The rows
-// of COMBINE_ROWS choices are loaded before the first is used, past the caches
-// (one row at a time 261 us; four at a time but cached 230 us).
+// with inputs and outputs that are in no cache, 32768 tokens x 8 rows of 2048
+// BF16 take 198 us (1.21 GB, 6.1 TB/s).  The rows of COMBINE_ROWS choices are
+// loaded before the first is used: with a load and its sum in turn 261 us.
+// Cached loads cost 213 us, cached stores 223 us, both 234 us.
 template <bool BF16, bool BF16_OUT>
 __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(
     const void *rows, int64_t total_rows, const int64_t *token_rows, const float *weights,
@@ -804,8 +807,9 @@ __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(
 }
 
 // d_rows[r] = w dout[t], d_weights = <dout[t], rows[r]>; the workgroups together
-// zero the rows past the last segment.  9001 tokens x 8 rows of 2048 BF16 take
-// 97 us (598 MB, 6.2 TB/s); with four rows in flight 104 us, with one 125 us.
+// zero the rows past the last segment.  9001 tokens x 8 rows of 2048 BF16, in no
+// cache, take 114 us (598 MB, 5.2 TB/s; a copy of 300 MiB reaches 5.4): with
+// cached loads 117 us, cached stores 124 us, with four rows in flight 122 us.
 template <bool BF16>
 __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_backward_kernel(
     const void *d_out, const void *rows, int64_t total_rows, const int64_t *token_rows,
