@@ -783,7 +783,7 @@ typedef struct {
  * Scores, the running maximum and sum and the output are fp32; q is held in
  * FP16 under a power-of-two scale per row (as BF16 activations above) and the
  * softmax's numerators, times the values' FP32 scales, in FP16 (2^-11
- * relative) down to 2^-54 of the row's largest.  A value row whose FP32 scale is below
+ * relative) as far down as 2^-130 of the row's largest.  A value row whose FP32 scale is below
  * 2^-100 counts as zeros; the others of a sequence must lie within 2^100 of
  * each other.
  */

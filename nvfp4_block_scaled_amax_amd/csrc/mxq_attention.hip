@@ -18,9 +18,9 @@
 // the numerators are 2^(z + log2 s_v - m + TOP), m the running maximum of
 // z + log2 s_v (to within SLACK).  They are rounded to FP16: the largest is
 // 2^11 to 2^15, and one within 2^-25 of it keeps all its 11 bits whatever
-// the scales are.  A step with smaller ones (whose values may be all that an output element is made
-// of, where the others' codes are 0) takes those in a second round of
-// products under 2^29.  The sum takes each numerator times 1 / s_v.  q is
+// the scales are.  A step with smaller ones (whose values may be all that an
+// output element is made of, where the others' codes are 0) takes those in
+// further rounds of products, under 2^29, 2^58 .. as far as FP32 reaches.  The sum takes each numerator times 1 / s_v.  q is
 // exact in FP16 under a power of two per row.
 //   Operand order.  A lane reads the D/4 consecutive elements of a key that
 // belong to its group (16 bytes at D = 128) and the queries are loaded in the
@@ -62,10 +62,14 @@ constexpr int ATT_WAVES = 4, ATT_THREADS = 64 * ATT_WAVES;
 constexpr int ATT_TILE = 32;                        // keys per step of a wavefront
 constexpr int ATT_MIN_CHUNK = 2 * ATT_TILE * ATT_WAVES;
 constexpr int ATT_TARGET = 640;                    // chunks a launch aims at
+constexpr int WIDE_WAVES = 8, WIDE_THREADS = 64 * WIDE_WAVES;       // many query rows: see below
+constexpr int WIDE_RT = 2, WIDE_ROWS = 16 * WIDE_RT * WIDE_WAVES;
+constexpr int WIDE_TARGET = 480;                   // chunks of its launch (232: 145 us, 1000: 144)
+constexpr int WIDE_TILES = 200;                    // least row tiles of 32 for it
 constexpr float NO_MAX = -1.0e30f;                  // running maximum before the first key
 constexpr float TOP = 11.0f, SLACK = 4.0f;          // numerators: 2^TOP at m, 2^15 at m + SLACK
-constexpr float LOW_LOG2 = -14.0f, LOW = 0x1p-14f;  // smaller ones go to the second round,
-constexpr float LOW_UP = 0x1p29f;                   // under this factor
+constexpr float LOW_LOG2 = -14.0f, LOW = 0x1p-14f;  // smaller ones go to further rounds,
+constexpr float LOW_UP = 0x1p29f;                   // each under this factor more
 constexpr float MIN_VS = 0x1p-100f;                 // value scales below count as 0
 constexpr int ATT_STAGES = 2;                      // tiles in LDS per wavefront
 
@@ -81,7 +85,7 @@ struct AttnK {
     Div page_div, group_div;
     float scale;                                     // softmax_scale * log2 e
     int causal, window;
-    int n_seqs, row_tiles, tile_rows;                // tile_rows = 16 RT
+    int n_seqs, row_tiles, tile_rows, target;        // target: chunks of the launch
     bool split;
     uint16_t *out;
     float *lse;
@@ -132,7 +136,7 @@ __device__ __forceinline__ int plan_chunk(const AttnK &a, int lane)
         keys += seq_span(a, seq_len(a, b));
     keys = wave_sum_i64(keys, lane) * a.n_kv_heads * a.row_tiles;
     constexpr int STEP = ATT_TILE * ATT_WAVES;
-    int64_t c = (keys / ATT_TARGET + STEP) / STEP * STEP;
+    int64_t c = (keys / a.target + STEP) / STEP * STEP;
     c = c < ATT_MIN_CHUNK ? ATT_MIN_CHUNK : c;
     return __builtin_amdgcn_readfirstlane((int)c);
 }
@@ -374,6 +378,181 @@ __device__ __forceinline__ T lds_ld(lds_cptr p)
     return *reinterpret_cast<__attribute__((address_space(3))) const T *>(p);
 }
 
+// Step kk of a lane's D/4 elements of a key, which hold D/64 blocks of 16 (two dwords
+// each).
+__device__ __forceinline__ f16x8_t key_f16(uint32_t codes, uint32_t blocks, int kk)
+{
+    const f16x2_t d = e4m3_pair_f16(blocks >> (16 * (kk / 4)));
+    const _Float16 dk = d[(kk / 2) & 1];
+    return oct_f16(codes, f16x2_t{dk, dk});
+}
+
+// Values as operands: pairs of keys (2i, 2i + 1) of the lane group's eight, their
+// codes merged (even and odd elements), and their block scales.
+template <int VW>
+struct ValuePairs {
+    f16x2_t vd[4];
+    uint32_t ev[4][VW], od[4][VW];
+    __device__ __forceinline__ ValuePairs(const uint32_t (&vc)[8][VW], const uint32_t (&vb)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            vd[i] = e4m3_pair_f16(vb[2 * i] | vb[2 * i + 1] << 8);
+#pragma unroll
+            for (int w = 0; w < VW; w++) {
+                const uint32_t c0 = vc[2 * i][w], c1 = vc[2 * i + 1][w];
+                ev[i][w] = (c0 & 0x0F0F0F0Fu) | ((c1 << 4) & 0xF0F0F0F0u);
+                od[i][w] = ((c0 >> 4) & 0x0F0F0F0Fu) | (c1 & 0xF0F0F0F0u);
+            }
+        }
+    }
+    // Element j of the lane's D/16, eight keys.
+    __device__ __forceinline__ f16x8_t operator()(int j) const
+    {
+        f16x2_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            v[i] = pair_f16_dyn((j & 1) ? od[i][j >> 3] : ev[i][j >> 3], (j >> 1) & 3) * vd[i];
+        return cat8(v[0], v[1], v[2], v[3]);
+    }
+    // The same, decoded anew where it is called: shared with the other uses, the
+    // decoded values would stay in registers.
+    __device__ __forceinline__ f16x8_t again(int j) const
+    {
+        f16x2_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            uint32_t c = (j & 1) ? od[i][j >> 3] : ev[i][j >> 3];
+            asm volatile("" : "+v"(c));
+            v[i] = pair_f16_dyn(c, (j >> 1) & 3) * vd[i];
+        }
+        return cat8(v[0], v[1], v[2], v[3]);
+    }
+};
+
+// lv = log2 s_v, rv = 2^-lv of the lane group's eight values, whose block scales are
+// vb.  A value scale of 0 (below MIN_VS) stands for a row of zeros, and slots past
+// the length may hold anything: their block scales count as 0, and they take
+// part in the sum under the largest scale beside them.
+template <bool MASKED>
+__device__ __forceinline__ void value_scales(const f32x4_t (&vs)[2], uint32_t (&vb)[8],
+                                             float (&lv)[8], float (&rv)[8], int t0, int len,
+                                             int g)
+{
+    float vmin = vs[0][0];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        lv[j] = vs[j >> 2][j & 3];
+        vmin = __builtin_fminf(vmin, lv[j]);
+    }
+    if (MASKED || __builtin_amdgcn_ballot_w64(vmin < MIN_VS) != 0) {
+        float vz = MIN_VS;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const bool live = lv[j] >= MIN_VS && t0 + 16 * (j >> 2) + 4 * g + (j & 3) < len;
+            vb[j] = live ? vb[j] : 0;
+            lv[j] = live ? lv[j] : 0.0f;
+            vz = __builtin_fmaxf(vz, lv[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            lv[j] = lv[j] > 0.0f ? lv[j] : vz;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        lv[j] = __builtin_amdgcn_logf(lv[j]);
+        rv[j] = __builtin_amdgcn_exp2f(-lv[j]);
+    }
+}
+
+// The softmax of a tile's scores s and its products with the values: value(j) are
+// the values' operands, again(j) the same for further rounds.
+template <int D, int RT, bool MASKED, typename Value, typename Again>
+__device__ __forceinline__ void weigh(Rows<D, RT> &st, const f32x4_t (&s)[2][RT],
+                                      const f32x4_t (&ks)[2], const float (&lv)[8],
+                                      const float (&rv)[8], int t0, const int (&lo)[RT],
+                                      const int (&hi)[RT], int g, Value value, Again again)
+{
+    f16x8_t p8[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        float z[8], zx = NO_MAX, zn = -NO_MAX;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            z[j] = __builtin_fmaf(s[j >> 2][rt][j & 3], ks[j >> 2][j & 3] * st.c[rt], lv[j]);
+            if constexpr (MASKED) {
+                const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
+                const bool see = t >= lo[rt] && t < hi[rt];
+                zn = __builtin_fminf(zn, see ? z[j] : -NO_MAX);
+                z[j] = see ? z[j] : NO_MAX;
+            } else {
+                zn = __builtin_fminf(zn, z[j]);
+            }
+            zx = __builtin_fmaxf(zx, z[j]);
+        }
+        // m follows the maximum only when that is past m + SLACK: with m exact, nearly
+        // every step of a short chunk had some row whose maximum rose.
+        zx = max4_groups(zx);
+        if (__builtin_amdgcn_ballot_w64(zx > st.m[rt] + SLACK) != 0) {
+            const float mn = zx > st.m[rt] + SLACK ? zx : st.m[rt];
+            const float al = __builtin_amdgcn_exp2f(st.m[rt] - mn);
+            st.m[rt] = mn;
+            st.l[rt] *= al;
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                st.o[rt][j] *= al;
+        }
+        const float base = st.m[rt] - TOP;
+        float p[8], sum[2] = {};
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            p[j] = __builtin_amdgcn_exp2f(z[j] - base);
+            if constexpr (MASKED)                    // a row that has seen no key: m = NO_MAX
+                p[j] = z[j] == NO_MAX ? 0.0f : p[j];
+            sum[j & 1] = __builtin_fmaf(p[j], rv[j], sum[j & 1]);
+        }
+        st.l[rt] += sum[0] + sum[1];
+        if (__builtin_amdgcn_ballot_w64(zn - base < LOW_LOG2) != 0) {
+            // Numerators in [bound / LOW_UP, bound), each round 29 bits further down.
+            float bound = LOW, up = LOW_UP, down = 1.0f / LOW_UP, bits = LOW_LOG2;
+#pragma unroll 1
+            do {
+                f16x8_t plo;
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    plo[j] = (_Float16)(p[j] < bound && p[j] >= bound * (1.0f / LOW_UP) ? p[j] * up
+                                                                                      : 0.0f);
+#pragma unroll
+                for (int j = 0; j < D / 16; j++) {
+                    const f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        again(j), plo, f32x4_t{}, 0, 0, 0);
+                    st.o[rt][j] += o * down;
+                    __builtin_amdgcn_sched_barrier(0);               // one at a time: registers
+                }
+                bound *= 1.0f / LOW_UP;
+                up *= LOW_UP;
+                down *= 1.0f / LOW_UP;
+                bits -= 29.0f;
+            } while (bits > -126.0f && __builtin_amdgcn_ballot_w64(zn - base < bits) != 0);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                p[j] = p[j] < LOW ? 0.0f : p[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            p8[rt][j] = (_Float16)p[j];
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; j++) {
+        const f16x8_t vf = value(j);
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++)
+            st.o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p8[rt], st.o[rt][j], 0, 0, 0);
+        if (j & 1)
+            __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // One step: the tile at LDS address x (keys t0 ..).
 template <int D, int RT, bool MASKED>
 __device__ __forceinline__ void attend(Rows<D, RT> &st, uint32_t x, int t0, int len,
@@ -415,10 +594,7 @@ __device__ __forceinline__ void attend(Rows<D, RT> &st, uint32_t x, int t0, int 
         f16x8_t kf[2];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            // The D/4 elements of a lane hold D/64 blocks of 16 (two dwords each).
-            const f16x2_t d = e4m3_pair_f16(kb[h] >> (16 * (kk / 4)));
-            const _Float16 dk = d[(kk / 2) & 1];
-            kf[h] = oct_f16(kc[h][kk], f16x2_t{dk, dk});
+            kf[h] = key_f16(kc[h][kk], kb[h], kk);
         }
 #pragma unroll
         for (int rt = 0; rt < RT; rt++)
@@ -453,165 +629,37 @@ __device__ __forceinline__ void attend(Rows<D, RT> &st, uint32_t x, int t0, int 
         }
         vb[j] = lds_ld<uint8_t>(pvb + key * (D / 16));
     }
-    // lv = log2 s_v, rv = 2^-lv.  A value scale of 0 (below MIN_VS) stands for a row of
-    // zeros, and slots past the length may hold anything: their block scales count
-    // as 0, and they take part in the sum under the largest scale beside them.
-    float lv[8], rv[8], vmin = vs[0][0];
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        lv[j] = vs[j >> 2][j & 3];
-        vmin = __builtin_fminf(vmin, lv[j]);
-    }
-    if (MASKED || __builtin_amdgcn_ballot_w64(vmin < MIN_VS) != 0) {
-        float vz = MIN_VS;
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const bool live = lv[j] >= MIN_VS && t0 + 16 * (j >> 2) + 4 * g + (j & 3) < len;
-            vb[j] = live ? vb[j] : 0;
-            lv[j] = live ? lv[j] : 0.0f;
-            vz = __builtin_fmaxf(vz, lv[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            lv[j] = lv[j] > 0.0f ? lv[j] : vz;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        lv[j] = __builtin_amdgcn_logf(lv[j]);
-        rv[j] = __builtin_amdgcn_exp2f(-lv[j]);
-    }
-    // Values: pairs of keys (2i, 2i + 1) of the lane group's eight.
-    f16x2_t vd[4];
-    uint32_t ev[4][VW], od[4][VW];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        vd[i] = e4m3_pair_f16(vb[2 * i] | vb[2 * i + 1] << 8);
-#pragma unroll
-        for (int w = 0; w < VW; w++) {
-            const uint32_t c0 = vc[2 * i][w], c1 = vc[2 * i + 1][w];
-            ev[i][w] = (c0 & 0x0F0F0F0Fu) | ((c1 << 4) & 0xF0F0F0F0u);
-            od[i][w] = ((c0 >> 4) & 0x0F0F0F0Fu) | (c1 & 0xF0F0F0F0u);
-        }
-    }
-    auto values = [&](int j) {
-        f16x2_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            v[i] = pair_f16_dyn((j & 1) ? od[i][j >> 3] : ev[i][j >> 3], (j >> 1) & 3) * vd[i];
-        return cat8(v[0], v[1], v[2], v[3]);
-    };
-    // The same, decoded anew where it is called: shared with the other uses, the
-    // decoded values would stay in registers.
-    auto values_again = [&](int j) {
-        f16x2_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            uint32_t c = (j & 1) ? od[i][j >> 3] : ev[i][j >> 3];
-            asm volatile("" : "+v"(c));
-            v[i] = pair_f16_dyn(c, (j >> 1) & 3) * vd[i];
-        }
-        return cat8(v[0], v[1], v[2], v[3]);
-    };
-    f16x8_t p8[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        float z[8], zx = NO_MAX, zn = -NO_MAX;
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            z[j] = __builtin_fmaf(s[j >> 2][rt][j & 3], ks[j >> 2][j & 3] * st.c[rt], lv[j]);
-            if constexpr (MASKED) {
-                const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                z[j] = t >= lo[rt] && t < hi[rt] ? z[j] : NO_MAX;
-            }
-            zx = __builtin_fmaxf(zx, z[j]);
-            zn = __builtin_fminf(zn, z[j]);
-        }
-        // m follows the maximum only when that is past m + SLACK: with m exact, nearly
-        // every step of a short chunk had some row whose maximum rose.
-        zx = max4_groups(zx);
-        if (__builtin_amdgcn_ballot_w64(zx > st.m[rt] + SLACK) != 0) {
-            const float mn = zx > st.m[rt] + SLACK ? zx : st.m[rt];
-            const float al = __builtin_amdgcn_exp2f(st.m[rt] - mn);
-            st.m[rt] = mn;
-            st.l[rt] *= al;
-#pragma unroll
-            for (int j = 0; j < D / 16; j++)
-                st.o[rt][j] *= al;
-        }
-        const float base = st.m[rt] - TOP;
-        float p[8], sum[2] = {};
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            p[j] = __builtin_amdgcn_exp2f(z[j] - base);
-            if constexpr (MASKED)                    // a row that has seen no key: m = NO_MAX
-                p[j] = z[j] == NO_MAX ? 0.0f : p[j];
-            sum[j & 1] = __builtin_fmaf(p[j], rv[j], sum[j & 1]);
-        }
-        st.l[rt] += sum[0] + sum[1];
-        if (__builtin_amdgcn_ballot_w64(zn - base < LOW_LOG2) != 0) {   // masked keys too: harmless
-            f16x8_t plo;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                plo[j] = (_Float16)(p[j] < LOW ? p[j] * LOW_UP : 0.0f);
-                p[j] = p[j] < LOW ? 0.0f : p[j];
-            }
-#pragma unroll
-            for (int j = 0; j < D / 16; j++) {
-                const f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_f16(values_again(j), plo,
-                                                                         f32x4_t{}, 0, 0, 0);
-                st.o[rt][j] += o * (1.0f / LOW_UP);
-                __builtin_amdgcn_sched_barrier(0);   // one at a time: registers
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            p8[rt][j] = (_Float16)p[j];
-    }
-#pragma unroll
-    for (int j = 0; j < D / 16; j++) {
-        const f16x8_t vf = values(j);
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++)
-            st.o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p8[rt], st.o[rt][j], 0, 0, 0);
-        if (j & 1)
-            __builtin_amdgcn_sched_barrier(0);
-    }
+    float lv[8], rv[8];
+    value_scales<MASKED>(vs, vb, lv, rv, t0, len, g);
+    const ValuePairs<VW> v(vc, vb);
+    weigh<D, RT, MASKED>(st, s, ks, lv, rv, t0, lo, hi, g, v, [&](int j) { return v.again(j); });
 }
 
-template <int D, int RT>
-__global__ void __launch_bounds__(ATT_THREADS, D * RT <= 128 ? 3 : 2)
-    nvfp4_attention_kernel(AttnK a)
+// What rows r0 .. r1 - 1 of a sequence of len keys see: keys [kmin, kmax) at most, of
+// which every row sees [full_lo, full_hi); kmin is a tile's first key.
+struct Span {
+    int kmin, kmax, full_lo, full_hi;
+};
+__device__ __forceinline__ Span row_span(const AttnK &a, int r0, int r1, int len)
 {
-    constexpr int ROWS = 16 * RT;
-    // The wavefronts' tiles; after the loop their sums: rows padded by four floats, so
-    // that the 16 rows a store touches miss each other's banks.
-    constexpr int TILE_BYTES = ATT_WAVES * ATT_STAGES * Stage<D>::BYTES;
-    constexpr int SUM_BYTES = ATT_WAVES * ROWS * (D + 4) * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t
-        lds[TILE_BYTES > SUM_BYTES ? TILE_BYTES : SUM_BYTES];
-    __shared__ float lds_ml[ATT_WAVES][ROWS][2];
-    float(*lds_o)[ROWS][D + 4] = reinterpret_cast<float(*)[ROWS][D + 4]>(lds);
-
-    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
-    Unit un;
-    if (!plan_unit(a, wg_id(), lane, &un))
-        return;
-    const int tile = un.tile, kvh = un.kvh, b = un.b, len = un.len;
-
-    // Keys the tile's rows see: [kmin, kmax); this workgroup's part of them.
-    const int r0 = tile * ROWS;
-    const int r1 = r0 + ROWS < a.rows ? r0 + ROWS : a.rows;
     const int first = len - a.q_len + (int)udiv((uint32_t)r0, a.group_div);
     const int last = len - a.q_len + (int)udiv((uint32_t)(r1 - 1), a.group_div);
-    const int kmax = a.causal ? (last + 1 < 0 ? 0 : last + 1) : len;
-    int kmin = a.causal && a.window > 0 ? first - a.window + 1 : 0;
-    kmin = kmin < 0 ? 0 : kmin & ~(ATT_TILE - 1);
-    const int64_t start64 = (int64_t)kmin + (int64_t)un.chunk * un.chunk_keys;
-    const int start = start64 < kmax ? (int)start64 : kmax;
-    const int stop = kmax - start < un.chunk_keys ? kmax : start + un.chunk_keys;
+    Span s;
+    s.kmax = a.causal ? (last + 1 < 0 ? 0 : last + 1) : len;
+    const int kmin = a.causal && a.window > 0 ? first - a.window + 1 : 0;
+    s.kmin = kmin < 0 ? 0 : kmin & ~(ATT_TILE - 1);
+    s.full_hi = a.causal ? (first + 1 < len ? first + 1 : len) : len;
+    s.full_lo = a.causal && a.window > 0 ? last - a.window + 1 : 0;
+    return s;
+}
 
-    Rows<D, RT> st;
-    int lo[RT], hi[RT];
+// Loads a wavefront's query rows r0 .. and starts their state; row (lane % 16) of
+// tile rt sees keys [lo, hi).
+template <int D, int RT>
+__device__ __forceinline__ void start_rows(const AttnK &a, Rows<D, RT> &st, int (&lo)[RT],
+                                           int (&hi)[RT], int r0, int b, int kvh, int len, int l,
+                                           int g)
+{
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
         const int r = r0 + 16 * rt + l < a.rows ? r0 + 16 * rt + l : a.rows - 1;
@@ -651,12 +699,42 @@ __global__ void __launch_bounds__(ATT_THREADS, D * RT <= 128 ? 3 : 2)
         for (int j = 0; j < D / 16; j++)
             st.o[rt][j] = f32x4_t{};
     }
+}
+
+template <int D, int RT>
+__global__ void __launch_bounds__(ATT_THREADS, D * RT <= 128 ? 3 : 2)
+    nvfp4_attention_kernel(AttnK a)
+{
+    constexpr int ROWS = 16 * RT;
+    // The wavefronts' tiles; after the loop their sums: rows padded by four floats, so
+    // that the 16 rows a store touches miss each other's banks.
+    constexpr int TILE_BYTES = ATT_WAVES * ATT_STAGES * Stage<D>::BYTES;
+    constexpr int SUM_BYTES = ATT_WAVES * ROWS * (D + 4) * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t
+        lds[TILE_BYTES > SUM_BYTES ? TILE_BYTES : SUM_BYTES];
+    __shared__ float lds_ml[ATT_WAVES][ROWS][2];
+    float(*lds_o)[ROWS][D + 4] = reinterpret_cast<float(*)[ROWS][D + 4]>(lds);
+
+    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
+    Unit un;
+    if (!plan_unit(a, wg_id(), lane, &un))
+        return;
+    const int tile = un.tile, kvh = un.kvh, b = un.b, len = un.len;
+
+    // Keys the tile's rows see, and this workgroup's part of them.
+    const int r0 = tile * ROWS;
+    const int r1 = r0 + ROWS < a.rows ? r0 + ROWS : a.rows;
+    const Span sp = row_span(a, r0, r1, len);
+    const int64_t start64 = (int64_t)sp.kmin + (int64_t)un.chunk * un.chunk_keys;
+    const int start = start64 < sp.kmax ? (int)start64 : sp.kmax;
+    const int stop = sp.kmax - start < un.chunk_keys ? sp.kmax : start + un.chunk_keys;
+
+    Rows<D, RT> st;
+    int lo[RT], hi[RT];
+    start_rows<D, RT>(a, st, lo, hi, r0, b, kvh, len, l, g);
 
     const int64_t *table = a.table + (int64_t)b * a.max_pages;
     constexpr int STEP = ATT_TILE * ATT_WAVES;
-    // Keys every row sees: a tile inside [full_lo, full_hi) needs no mask.
-    const int full_hi = a.causal ? (first + 1 < len ? first + 1 : len) : len;
-    const int full_lo = a.causal && a.window > 0 ? last - a.window + 1 : 0;
     int t0 = start + wave * ATT_TILE;
     if (t0 < stop) {
         // Tiles go round ATT_STAGES buffers.  Steps past the last copy the last tile
@@ -689,7 +767,7 @@ __global__ void __launch_bounds__(ATT_THREADS, D * RT <= 128 ? 3 : 2)
         };
         // Loops of their own for tiles that need no mask and for the others: both
         // forms in one loop took 90 registers more.
-        auto full = [&] { return t0 >= full_lo && t0 + ATT_TILE <= full_hi; };
+        auto full = [&] { return t0 >= sp.full_lo && t0 + ATT_TILE <= sp.full_hi; };
         while (t0 <= t_last) {
             while (t0 <= t_last && full())
                 step(std::false_type{});
@@ -766,6 +844,249 @@ __global__ void __launch_bounds__(ATT_THREADS, D * RT <= 128 ? 3 : 2)
                 for (int h = 0; h < 2; h++)
                     *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + d + 4 * h) =
                         f32x4_t{o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]};
+        }
+    }
+}
+
+// Many query rows of 64 elements (chunks of a prompt).  A workgroup of eight
+// wavefronts takes WIDE_ROWS rows, and a step's four tiles are decoded once for all
+// of them: wavefronts 0 to 3 decode the keys of one tile each, 4 to 7 the values,
+// and leave them in LDS as the operands of the products, a lane's 16 bytes
+// after another's.  The next step's codes are loaded to registers meanwhile.
+// 3 chunks of 509 queries of 16 heads over up to 8192 keys: 118 us and 22 us for the
+// join, against 182 us where every 32 rows decode the keys anew; the issue of
+// vector instructions is what bounds both (62 % of the cycles here).  With
+// 128 registers for four wavefronts a SIMD instead of two it spills: 191 us.
+// Rows of 128 elements have fewer decodings per product and gain nothing (120
+// against 116 us for 4 chunks of 200 queries over 4000 keys).
+template <int D>
+struct Decoded {
+    static constexpr int KF = D / 16, VF = D / 16;   // operands of 1 KiB
+    static constexpr int K = 0, V = 1024 * KF, KS = V + 1024 * VF, LV = KS + 128, RV = LV + 128,
+                         BYTES = RV + 128;
+};
+
+// A wavefront's part of a tile as loaded.  Keys: c[h KK + kk], b[h] of half h, s[0][0]
+// the FP32 scale of key lane % 32.  Values: c[j], b[j] of key j of the lane
+// group's eight, s their FP32 scales.
+template <int D>
+struct RawPart {
+    static constexpr int KK = D / 32;
+    uint32_t c[8], b[8];
+    f32x4_t s[2];
+
+    __device__ __forceinline__ void load_keys(const AttnK &a, const TileRows &rows, int lane)
+    {
+        const int l = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int64_t r = rows.r[h] + l;
+            const uint8_t *pc = a.k + r * (D / 2) + g * (D / 8);
+            const uint8_t *pb = a.kbs + r * (D / 16) + g * (D / 64);
+            const uint2 w = ld8(pc);
+            c[2 * h] = w.x;
+            c[2 * h + 1] = w.y;
+            b[h] = *pb;
+        }
+        s[0][0] = a.ks[(lane & 16 ? rows.r[1] : rows.r[0]) + l];
+    }
+    __device__ __forceinline__ void load_values(const AttnK &a, const TileRows &rows, int lane)
+    {
+        const int l = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int64_t r = rows.r[j >> 2] + 4 * g + (j & 3);
+            c[j] = *reinterpret_cast<const uint16_t *>(a.v + r * (D / 2) + l * (D / 32));
+            b[j] = a.vbs[r * (D / 16) + l * (D / 16) / 16];
+            s[j >> 2][j & 3] = a.vs[r];
+        }
+    }
+    __device__ __forceinline__ void decode_keys(uint8_t *out, int lane) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int kk = 0; kk < KK; kk++)
+                *reinterpret_cast<f16x8_t *>(out + Decoded<D>::K + 1024 * (h * KK + kk) +
+                                             16 * lane) = key_f16(c[h * KK + kk], b[h], kk);
+        if (lane < 32)
+            *reinterpret_cast<float *>(out + Decoded<D>::KS + 4 * lane) = s[0][0];
+    }
+    template <bool MASKED>
+    __device__ __forceinline__ void decode_values(uint8_t *out, int t0, int len, int lane)
+    {
+        const int g = lane >> 4;
+        float lv[8], rv[8];
+        value_scales<MASKED>(s, b, lv, rv, t0, len, g);
+        uint32_t codes[8][1];
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            codes[j][0] = c[j];
+        const ValuePairs<1> v(codes, b);
+#pragma unroll
+        for (int j = 0; j < D / 16; j++)
+            *reinterpret_cast<f16x8_t *>(out + Decoded<D>::V + 1024 * j + 16 * lane) = v(j);
+        if ((lane & 15) == 0)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                *reinterpret_cast<f32x4_t *>(out + Decoded<D>::LV + 64 * h + 16 * g) =
+                    f32x4_t{lv[4 * h], lv[4 * h + 1], lv[4 * h + 2], lv[4 * h + 3]};
+                *reinterpret_cast<f32x4_t *>(out + Decoded<D>::RV + 64 * h + 16 * g) =
+                    f32x4_t{rv[4 * h], rv[4 * h + 1], rv[4 * h + 2], rv[4 * h + 3]};
+            }
+    }
+};
+
+// One decoded tile (keys t0 ..) and a wavefront's rows.
+template <int D, int RT, bool MASKED>
+__device__ __forceinline__ void attend_decoded(Rows<D, RT> &st, const uint8_t *x, int t0,
+                                               const int (&lo)[RT], const int (&hi)[RT], int lane)
+{
+    using De = Decoded<D>;
+    constexpr int KK = D / 32;
+    const int g = lane >> 4;
+    const uint32_t x32 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)x;
+    const lds_cptr mine = lds_at(x32 + 16 * lane), group = lds_at(x32 + De::KS + 16 * g);
+    f32x4_t s[2][RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++)
+        s[0][rt] = s[1][rt] = f32x4_t{};
+#pragma unroll
+    for (int kk = 0; kk < KK; kk++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const f16x8_t kf = lds_ld<f16x8_t>(mine + De::K + 1024 * (h * KK + kk));
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+                s[h][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, st.q[rt][kk], s[h][rt], 0,
+                                                                  0, 0);
+        }
+    f32x4_t ks[2];
+    float lv[8], rv[8];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        ks[h] = lds_ld<f32x4_t>(group + 64 * h);
+        const f32x4_t vl = lds_ld<f32x4_t>(group + (De::LV - De::KS) + 64 * h);
+        const f32x4_t vr = lds_ld<f32x4_t>(group + (De::RV - De::KS) + 64 * h);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            lv[4 * h + i] = vl[i];
+            rv[4 * h + i] = vr[i];
+        }
+    }
+    // Further rounds read the values again: kept, they would take registers.
+    weigh<D, RT, MASKED>(
+        st, s, ks, lv, rv, t0, lo, hi, g,
+        [&](int j) { return lds_ld<f16x8_t>(mine + De::V + 1024 * j); },
+        [&](int j) { return lds_ld<f16x8_t>(lds_at(x32 + 16 * lane) + De::V + 1024 * j); });
+}
+
+template <int D>
+__global__ void __launch_bounds__(WIDE_THREADS, 2) nvfp4_attention_wide_kernel(AttnK a)
+{
+    constexpr int RT = WIDE_RT, STEP = ATT_TILE * ATT_WAVES;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[ATT_WAVES * Decoded<D>::BYTES];
+    const int lane = (int)lane_id(), l = lane & 15, g = lane >> 4, wave = wave_in_group();
+    Unit un;
+    if (!plan_unit(a, wg_id(), lane, &un))
+        return;
+    const int kvh = un.kvh, b = un.b, len = un.len;
+    const int r0 = un.tile * WIDE_ROWS;
+    const int r1 = r0 + WIDE_ROWS < a.rows ? r0 + WIDE_ROWS : a.rows;
+    const Span sp = row_span(a, r0, r1, len);
+    const int64_t start64 = (int64_t)sp.kmin + (int64_t)un.chunk * un.chunk_keys;
+    const int start = start64 < sp.kmax ? (int)start64 : sp.kmax;
+    const int stop = sp.kmax - start < un.chunk_keys ? sp.kmax : start + un.chunk_keys;
+
+    Rows<D, RT> st;
+    int lo[RT], hi[RT];
+    const int w0 = r0 + 16 * RT * wave;              // the wavefront's first row
+    start_rows<D, RT>(a, st, lo, hi, w0, b, kvh, len, l, g);
+
+    if (start < stop) {                              // the same for the whole workgroup
+        const int64_t *table = a.table + (int64_t)b * a.max_pages;
+        const int steps = (stop - start + STEP - 1) / STEP;
+        const bool values = wave >= ATT_WAVES;
+        const int part = ATT_TILE * (wave & (ATT_WAVES - 1));
+        const int t_last = start + part + (steps - 1) * STEP;
+        uint8_t *out = lds + (wave & (ATT_WAVES - 1)) * Decoded<D>::BYTES;
+        RowWindow win = row_window(a, table, kvh, start + part, STEP, t_last, lane);
+        RawPart<D> raw;
+        auto load = [&](int i) {
+            const TileRows rows = window_rows(win, i);
+            values ? raw.load_values(a, rows, lane) : raw.load_keys(a, rows, lane);
+        };
+        load(0);
+        int t = start, ahead = 1;                    // place in the window of the next load
+        auto step = [&](auto masked) {
+            constexpr bool MASKED = decltype(masked)::value;
+            __syncthreads();                         // the last step's tiles have been read
+            if (values)
+                raw.template decode_values<MASKED>(out, t + part, len, lane);
+            else
+                raw.decode_keys(out, lane);
+            if (ahead == 64) {
+                const int tn = t + part + STEP;
+                win = row_window(a, table, kvh, tn < t_last ? tn : t_last, STEP, t_last, lane);
+                ahead = 0;
+            }
+            load(ahead);                             // past the last step: the last tile again
+            ahead++;
+            __syncthreads();
+#pragma unroll 1
+            for (int i = 0; i < ATT_WAVES; i++) {
+                const int t0 = t + ATT_TILE * i;
+                if (t0 >= stop)
+                    break;
+                attend_decoded<D, RT, MASKED>(st, lds + i * Decoded<D>::BYTES, t0, lo, hi, lane);
+            }
+            t += STEP;
+        };
+        auto full = [&] { return t >= sp.full_lo && t + STEP <= sp.full_hi; };
+        while (t < stop) {
+            while (t < stop && full())
+                step(std::false_type{});
+            while (t < stop && !full())
+                step(std::true_type{});
+        }
+    }
+
+    // A lane holds, of row l of tile rt, elements (4g + i) D/16 + j.
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const float sum = sum4_groups(st.l[rt]), m = st.m[rt];
+        const int r = w0 + 16 * rt + l;
+        if (r >= r1)
+            continue;
+        if (un.n_chunks == 1) {
+            const int qi = (int)udiv((uint32_t)r, a.group_div);
+            const int64_t qrow = ((int64_t)b * a.q_len + qi) * a.n_heads + kvh * a.group +
+                                 (r - qi * a.group);
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                uint32_t v[D / 32];
+#pragma unroll
+                for (int j = 0; j < D / 32; j++)
+                    v[j] = (uint32_t)bf16_rne(st.o[rt][2 * j][i] * inv) |
+                           (uint32_t)bf16_rne(st.o[rt][2 * j + 1][i] * inv) << 16;
+                *reinterpret_cast<u32x2_t *>(a.out + qrow * D + (4 * g + i) * (D / 16)) =
+                    u32x2_t{v[0], v[1]};
+            }
+            if (a.lse && g == 0)
+                a.lse[qrow] = sum > 0.0f ? (m - TOP + __builtin_amdgcn_logf(sum)) * LN2
+                                         : -__builtin_inff();
+        } else {
+            const int64_t pr = (int64_t)wg_id() * WIDE_ROWS + (r - r0);
+            if (g == 0) {
+                a.part_ml[2 * pr] = m;
+                a.part_ml[2 * pr + 1] = sum;
+            }
+            if (sum > 0.0f)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    *reinterpret_cast<f32x4_t *>(a.part_o + pr * D + (4 * g + i) * (D / 16)) =
+                        f32x4_t{st.o[rt][0][i], st.o[rt][1][i], st.o[rt][2][i], st.o[rt][3][i]};
         }
     }
 }
@@ -847,7 +1168,7 @@ __global__ void __launch_bounds__(256) nvfp4_attention_join_kernel(AttnK a)
 // Row tiles of a launch, and the most units its plan can have: a chunk more
 // per (sequence, head, row tile) than its share of ATT_TARGET.
 struct AttnPlan {
-    int rt, row_tiles;
+    int rt, row_tiles, tile_rows, target;            // rt = 0: the kernel for many rows
     bool split;
     int64_t units;
 };
@@ -855,17 +1176,21 @@ AttnPlan attention_plan(int64_t n_seqs, int64_t q_len, int64_t n_heads, int64_t 
                         int64_t head_dim, int64_t max_keys)
 {
     const int64_t rows = q_len * (n_heads / n_kv_heads);
-    // More rows share a key's decoding, as far as a wavefront's registers go without
-    // spilling: 32 rows of 64 or 128 elements, 16 of 256.  (64 rows of 64 elements:
-    // 202 us against 176 us on chunks of 509 queries over 8192 keys.)
-    const int rt = rows <= 16 || head_dim == 256 ? 1 : 2;
-    const int64_t row_tiles = (rows + 16 * rt - 1) / (16 * rt);
+    // The kernel for many rows where they fill the chip: 224 tiles of 32 rows over
+    // 2000 keys take 42 us against 48, but 36 tiles over 4000 keys 40 us against 34.
+    const bool wide = head_dim == 64 && rows > 32 &&
+                      n_seqs * n_kv_heads * ((rows + 31) / 32) >= WIDE_TILES;
+    // Otherwise, more rows share a key's decoding as far as a wavefront's registers go
+    // without spilling: 32 rows of 64 or 128 elements, 16 of 256.
+    const int rt = wide ? 0 : rows <= 16 || head_dim == 256 ? 1 : 2;
+    const int tile_rows = wide ? WIDE_ROWS : 16 * rt, target = wide ? WIDE_TARGET : ATT_TARGET;
+    const int64_t row_tiles = (rows + tile_rows - 1) / tile_rows;
     const int64_t base = n_seqs * n_kv_heads * row_tiles;
     // With enough row tiles to fill the chip, or keys for one chunk, none is split.
-    const bool split = base < ATT_TARGET && max_keys > ATT_MIN_CHUNK;
+    const bool split = base < target && max_keys > ATT_MIN_CHUNK;
     const int64_t most = base * ((max_keys + ATT_MIN_CHUNK - 1) / ATT_MIN_CHUNK);
-    const int64_t units = !split ? base : most < ATT_TARGET + base ? most : ATT_TARGET + base;
-    return AttnPlan{rt, (int)row_tiles, split, units};
+    const int64_t units = !split ? base : most < target + base ? most : target + base;
+    return AttnPlan{rt, (int)row_tiles, tile_rows, target, split, units};
 }
 
 }  // namespace
@@ -874,7 +1199,7 @@ int64_t nvfp4_attention_workspace(int64_t n_seqs, int64_t q_len, int64_t n_heads
                                   int64_t n_kv_heads, int64_t head_dim, int64_t max_keys)
 {
     const AttnPlan p = attention_plan(n_seqs, q_len, n_heads, n_kv_heads, head_dim, max_keys);
-    return p.split ? p.units * 16 * p.rt * (head_dim + 2) * 4 : 0;
+    return p.split ? p.units * p.tile_rows * (head_dim + 2) * 4 : 0;
 }
 
 template <int D, int RT>
@@ -897,10 +1222,13 @@ hipError_t launch_nvfp4_attention(const AttnArgs &a, void *workspace, hipStream_
                   (int)a.page_size, (int)(a.q_len * group), make_div((uint32_t)a.page_size),
                   make_div((uint32_t)group), a.scale * LOG2E, a.causal ? 1 : 0,
                   (int)(a.window < 0x7FFFFFFF ? a.window : 0x7FFFFFFF), (int)a.n_seqs,
-                  p.row_tiles, 16 * p.rt, p.split, a.out, a.lse, ml,
-                  p.split ? ml + p.units * 16 * p.rt * 2 : nullptr};
+                  p.row_tiles, p.tile_rows, p.target, p.split, a.out, a.lse, ml,
+                  p.split ? ml + p.units * p.tile_rows * 2 : nullptr};
     const int64_t wgs = p.units;
-    if (a.head_dim == 64)
+    if (p.rt == 0)
+        hipLaunchKernelGGL(nvfp4_attention_wide_kernel<64>, dim3((unsigned)wgs),
+                           dim3(WIDE_THREADS), 0, stream, k);
+    else if (a.head_dim == 64)
         p.rt == 1 ? attention_launch<64, 1>(k, wgs, stream)
                   : attention_launch<64, 2>(k, wgs, stream);
     else if (a.head_dim == 128)

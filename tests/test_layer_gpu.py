@@ -565,6 +565,28 @@ def test_attention(lens, Q, H, Hkv, D, page):
     check_attention(attention_case(rng, lens, Q, H, Hkv, D, page), Hkv, page, "causal")
 
 
+@pytest.mark.parametrize("lens,Q,H,Hkv,page,causal,window", [
+    ([300, 201], 200, 16, 16, 16, True, 0), ([700, 64, 0], 70, 64, 32, 48, True, 0),
+    ([520, 33], 100, 32, 32, 32, True, 40), ([260, 130], 100, 40, 20, 16, False, 0),
+])
+def test_attention_many_rows(lens, Q, H, Hkv, page, causal, window):
+    """Enough query rows of 64 elements to fill the chip, in one part and in several,
+    some of them before the first key; slots past the length hold anything."""
+    rng = np.random.default_rng(53)
+    q, k, v, table, lens = case = attention_case(rng, lens, Q, H, Hkv, 64, page)
+    r = check_attention(case, Hkv, page, "many rows", causal=causal, window=window)
+    live = np.zeros(k[0].shape[0], bool)
+    for b, n in enumerate(lens):
+        t = np.arange(n)
+        for h in range(Hkv):
+            live[(table[b][t // page] * Hkv + h) * page + t % page] = True
+    for c, bs, s in (k, v):
+        c[~live], bs[~live], s[~live] = 0xFF, 0x7F, np.nan
+    again = run_attention(q, k, v, table, lens, Hkv, page, None, causal, window)
+    torch.cuda.synchronize()
+    assert torch.equal(again.out, r.out) and torch.equal(again.lse, r.lse)
+
+
 @pytest.mark.parametrize("window", [1, 5, 16, 100])
 def test_attention_window(window):
     rng = np.random.default_rng(window)
