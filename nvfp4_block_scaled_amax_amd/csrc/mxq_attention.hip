@@ -262,10 +262,11 @@ struct Stage {
 };
 
 // Copies of 16 or 4 bytes a lane from per-lane addresses to LDS bytes lds + 16 lane
-// (4 lane).  The compiler does not track them: the loop counts them.
+// (4 lane).  The compiler does not track them: the loop counts them, and the wait
+// state that the copy needs after the write of M0 is the s_nop.
 __device__ __forceinline__ void to_lds16(const uint8_t *p, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                  :
                  : "v"(p), "s"(lds)
                  : "memory", "m0");
@@ -273,14 +274,14 @@ __device__ __forceinline__ void to_lds16(const uint8_t *p, uint32_t lds)
 // The same from a wave-uniform base and a lane's offset.
 __device__ __forceinline__ void to_lds16(const uint8_t *base, uint32_t off, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
                  : "v"(off), "s"(base), "s"(lds)
                  : "memory", "m0");
 }
 __device__ __forceinline__ void to_lds4(const uint8_t *p, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                  :
                  : "v"(p), "s"(lds)
                  : "memory", "m0");

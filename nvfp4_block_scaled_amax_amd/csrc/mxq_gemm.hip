@@ -139,17 +139,19 @@ __device__ __forceinline__ MxgOffsets mxg_offsets(int64_t m0, int64_t n0, int64_
 // later steps' copies (it cannot tell the buffers apart and would wait for
 // all of them); the kernel orders them itself: every wavefront waits for
 // its own copies of a step (a vmcnt that leaves only the later steps'
-// copies outstanding) before the barrier that publishes it.
+// copies outstanding) before the barrier that publishes it.  A copy needs one
+// wait state after the scalar write of M0; the compiler puts none into
+// assembly, so the s_nop is here.
 __device__ __forceinline__ void lds_copy16(const uint8_t *base, uint32_t off, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
                  : "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory", "m0");
 }
 __device__ __forceinline__ void lds_copy4(const uint8_t *base, uint32_t off, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                  :
                  : "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory", "m0");
