@@ -1,8 +1,14 @@
 """Tensor-level helpers over the C ABI: allocate outputs with torch.empty on
 the input's device and call the library.  BF16 inputs may be torch.bfloat16 or
-int16/uint16 tensors of bit patterns; they must be contiguous HIP tensors."""
+int16/uint16 tensors of bit patterns; they must be contiguous HIP tensors.
+
+`stream` (by default the current one) is where a call's kernels run.  Its
+outputs are memory of the current stream, as any tensor made there, so a caller
+that names another stream orders the two and keeps inputs and outputs until
+the kernels have run; what a call holds besides belongs to `stream` itself."""
 from __future__ import annotations
 
+import contextlib
 from typing import NamedTuple, Optional
 
 import torch
@@ -422,8 +428,24 @@ def _arg(t, what: str, dtype, shape):
     return t
 
 
-def _workspace(nbytes: int, like):
-    return _empty((nbytes,), torch.uint8, like) if nbytes else None
+def _on(stream):
+    """What a call allocates for itself and lets go on return belongs to the
+    stream that its kernels run on: memory of another stream could go to that
+    stream's next allocation while they still use it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _workspace(nbytes: int, like, stream):
+    if not nbytes:
+        return None
+    if stream is None:
+        return _empty((nbytes,), torch.uint8, like)
+    with _on(stream):
+        return _empty((nbytes,), torch.uint8, like)
 
 
 class Routing(NamedTuple):
@@ -454,7 +476,7 @@ def moe_route(logits, top_k: int, bias=None, scoring: int = B.MXQ_SCORE_SOFTMAX,
         rt = _empty((T * top_k,), torch.int64, logits)
         seg = _empty((E + 1,), torch.int64, logits)
         nbytes = B.mxq_moe_route_workspace(T, E)
-        ws = _workspace(nbytes, logits)
+        ws = _workspace(nbytes, logits, stream)
     params = B.mxq_route_params(top_k, n_expert_groups, topk_groups, group_topk, scoring,
                                 int(renormalize), scale)
     B.mxq_moe_route(code, logits, bias, T, E, params, w, e, tr, rt, seg, ws, nbytes, stream)
@@ -590,9 +612,10 @@ def nvfp4_expert_layer(x, routing: Routing, gateup: GateUpNVFP4, down: GateUpNVF
     SwiGLU, down, and the weighted return to the tokens.  x [T][K] BF16, FP32
     or NVFP4; gateup and down as nvfp4_quantize_gateup_pair exports them (down
     with up=None).  Intermediates are FP32; returns BF16 [T][N]."""
-    h = nvfp4_expert_gateup(x, gateup, routing.row_tokens, routing.seg_offsets, stream=stream)
-    y = nvfp4_expert_matvec(h, down.gate_codes, down.gate_block_scales, down.scope_scales,
-                            routing.seg_offsets, stream=stream)
+    with _on(stream):
+        h = nvfp4_expert_gateup(x, gateup, routing.row_tokens, routing.seg_offsets, stream=stream)
+        y = nvfp4_expert_matvec(h, down.gate_codes, down.gate_block_scales, down.scope_scales,
+                                routing.seg_offsets, stream=stream)
     return moe_combine(y, routing.token_rows, routing.weights, torch.bfloat16, stream)
 
 
@@ -651,5 +674,5 @@ def nvfp4_attention(q, k: NVFP4, v: NVFP4, block_table, seq_lens, n_kv_heads: in
                                              max_pages * page_size)
     B.mxq_nvfp4_attention(q, k, v, block_table, seq_lens, n_seqs, q_len, n_heads, n_kv_heads, D,
                           n_rows // per_page, page_size, max_pages, scale, causal, window, out,
-                          lse, _workspace(nbytes, q), nbytes, stream)
+                          lse, _workspace(nbytes, q, stream), nbytes, stream)
     return Attention(out, lse)

@@ -1,0 +1,59 @@
+"""The layer operators on the GPU at the edges of their ranges, against the
+64-bit forms of layer_ref with the tolerances of test_layer_gpu."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as R
+import nvfp4_block_scaled_amax_amd as mxq
+from nvfp4_block_scaled_amax_amd import api
+from nvfp4_block_scaled_amax_amd import workloads as W
+from gpu_util import announce, dev, require_gpu
+from test_layer_gpu import attention_case, bf16, put
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+# ---------------------------------------------------------------------------
+# A stream named in the call
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_named_stream_keeps_what_the_call_lets_go(raw):
+    """The side stream is busy when the calls return; what the current stream
+    allocates and fills meanwhile must not be what they still use."""
+    rng = np.random.default_rng(61)
+    T, E, k, H, I = 200, 16, 4, 256, 128
+    x = put(bf16(rng.normal(0, 1, (T, H))), torch.bfloat16)
+    lg = put(rng.normal(0, 1, (T, E)), torch.float32)
+    pair = api.nvfp4_quantize_gateup_pair(*(dev(W.bf16_bits(rng.normal(0, 0.05, (E, I, H))))
+                                            for _ in range(2)))
+    dn = api.nvfp4_quantize_gateup_pair(dev(W.bf16_bits(rng.normal(0, 0.05, (E, H, I)))))
+    r = api.moe_route(lg, k)
+    q, kc, vc, table, lens = attention_case(rng, [700, 300], 1, 8, 2, 64, 16)
+    q, table, lens = put(q, torch.bfloat16), dev(table), dev(lens)
+    kc, vc = api.NVFP4(*(dev(a) for a in kc)), api.NVFP4(*(dev(a) for a in vc))
+    calls = [lambda s: tuple(api.moe_route(lg, k, stream=s)),
+             lambda s: (api.nvfp4_expert_layer(x, r, pair, dn, stream=s),),
+             lambda s: tuple(api.nvfp4_attention(q, kc, vc, table, lens, 2, 16, stream=s))]
+    side = torch.cuda.Stream()
+    for i, f in enumerate(calls):
+        announce(f"named stream, call {i}")
+        want = f(None)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = f(side.cuda_stream if raw else side)
+        # Sizes of the temporaries: the workspaces, and h and y of the expert layer.
+        taken = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")
+                 for n in (mxq.mxq_moe_route_workspace(T, E), T * k * I * 4, T * k * H * 4,
+                           mxq.mxq_nvfp4_attention_workspace(2, 1, 8, 2, 64, 704))]
+        torch.cuda.synchronize()
+        assert all(bool((t == 0x5A).all()) for t in taken), i
+        for a, b in zip(want, got):
+            assert torch.equal(a, b), i
