@@ -141,10 +141,12 @@ __device__ __forceinline__ T best_key(const T (&key)[V], int l, int *index)
     return m;
 }
 
-// Chooses the experts of a token from its logits x (none: never selected):
-// lane c of its L lanes gets choice c, -1 where none is left.  lds: room for the
-// keys of a token (groups).  Returns whether the keys' error leaves no doubt
-// (always in 64 bits); den is the softmax's sum under the largest logit m.
+// Chooses the experts of a token from its logits x (none: never selected, a
+// score of 0) and biases (none: never selected, its score a term of the
+// softmax's sum like any other): lane c of its L lanes gets choice c, -1 where
+// none is left.  lds: room for the keys of a token (groups).  Returns whether
+// the keys' error leaves no doubt (always in 64 bits); den is the softmax's
+// sum under the largest logit m.
 template <bool BY_LOGIT, int L, int V, typename T>
 __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V],
                                        const float (&bias)[V], int l, T *lds, int *chosen,
@@ -355,12 +357,11 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(RouteArgs a)
             bias[j] = 0.0f;
             if (e < E) {
                 f = ld_elem<BF16>(a.logits, t * E + e);
-                bool out = is_masked(f);
+                f = is_masked(f) ? -__builtin_inff() : f;
                 if (a.bias) {
                     bias[j] = a.bias[e];
-                    out = out || is_masked(bias[j]);
+                    bias[j] = is_masked(bias[j]) ? -__builtin_inff() : bias[j];
                 }
-                f = out ? -__builtin_inff() : f;
                 f = f < 3.402823466e+38f ? f : 3.402823466e+38f;
             }
             x[j] = f;

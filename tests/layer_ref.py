@@ -29,8 +29,6 @@ def route(x, bias, p):
     """x [T][E] float64 -> (weights float64, experts, token_rows, row_tokens, seg)."""
     T, E = x.shape
     dead = ~(x > -np.inf)                       # -inf and NaN
-    if bias is not None:
-        dead |= ~(bias > -np.inf)[None, :]
     x = np.where(dead, -np.inf, np.minimum(x, np.finfo(np.float32).max))
     with np.errstate(over="ignore", invalid="ignore"):
         if p["scoring"] == 1:
@@ -40,6 +38,8 @@ def route(x, bias, p):
             s = np.where(dead, 0.0, np.exp(np.where(dead, 0.0, x - np.where(m > -np.inf, m, 0))))
             t = s.sum(1, keepdims=True)
             s = s / np.where(t > 0, t, 1.0)
+    if bias is not None:                        # disabled: no key, but a term of the softmax's sum
+        dead = dead | ~(bias > -np.inf)[None, :]
     by_logit = bias is None and (p["n_groups"] == 1 or p["group_topk"] == 1)
     key = x if by_logit else np.where(dead, -np.inf, s + (0.0 if bias is None else bias[None, :]))
     G, k = p["n_groups"], p["top_k"]

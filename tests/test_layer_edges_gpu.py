@@ -57,3 +57,34 @@ def test_named_stream_keeps_what_the_call_lets_go(raw):
         assert all(bool((t == 0x5A).all()) for t in taken), i
         for a, b in zip(want, got):
             assert torch.equal(a, b), i
+
+
+# ---------------------------------------------------------------------------
+# Routing
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k", [(7, 24, 4), (70, 24, 4), (40, 300, 20)])
+def test_a_disabled_expert_stays_in_the_softmax(T, E, k, dtype):
+    """The bias moves the selection only: with experts at a bias of -inf (or NaN),
+    the likeliest among them, the others keep the scores of the softmax over all
+    experts, in the keys and in the weights."""
+    announce(f"disabled experts {T}x{E} {dtype}")
+    rng = np.random.default_rng(T + E)
+    x = rng.normal(0, 1.5, (T, E))
+    x[:, 0] += 4.0
+    x = bf16(x) if dtype == torch.bfloat16 else x.astype(np.float32).astype(np.float64)
+    b = rng.normal(0, 0.05, E).astype(np.float32).astype(np.float64)
+    b[::5] = -np.inf
+    b[5] = np.nan
+    r = api.moe_route(put(x, dtype), k, bias=put(b, torch.float32), renormalize=False)
+    torch.cuda.synchronize()
+    s = R.scores(x, mxq.MXQ_SCORE_SOFTMAX)
+    key = np.where(b > -np.inf, s + np.where(b > -np.inf, b, 0.0), -np.inf)
+    want = np.argsort(-key, 1, kind="stable")[:, :k]
+    assert np.array_equal(r.experts.cpu().numpy(), want)
+    w = np.take_along_axis(s, want, 1)
+    got = r.weights.cpu().double().numpy()
+    assert (np.abs(got - w) <= w * 2.0 ** -20).all()
+    # The function whose gradient moe_route_backward gives.
+    assert np.array_equal(w, R.route_weights(x, want, mxq.MXQ_SCORE_SOFTMAX, False, 1.0))
