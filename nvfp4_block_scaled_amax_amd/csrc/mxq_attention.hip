@@ -104,8 +104,8 @@ __device__ __forceinline__ int seq_span(const AttnK &a, int len)
     if (!a.causal || a.window == 0)
         return len;
     // The tile's first row reaches back window - 1 keys, rounded down to a tile.
-    const int64_t w = (int64_t)a.window + a.tile_rows + ATT_TILE;
-    return w < len ? (int)w : len;
+    const int w = a.window + a.tile_rows + ATT_TILE;
+    return w < len ? w : len;
 }
 
 __device__ __forceinline__ int wave_scan(int v, int lane)       // inclusive
@@ -1218,13 +1218,14 @@ hipError_t launch_nvfp4_attention(const AttnArgs &a, void *workspace, hipStream_
     const int64_t n_rows = a.n_seqs * a.q_len * a.n_heads;
     float *ml = static_cast<float *>(workspace);
     const int group = (int)(a.n_heads / a.n_kv_heads);
+    // A window of all keys and queries is none, and positions less it fit 32 bits.
+    const int64_t most = max_keys + a.q_len, window = a.window < most ? a.window : most;
     const AttnK k{a.q, a.k, a.kbs, a.ks, a.v, a.vbs, a.vs, a.block_table, a.seq_lens, a.n_pages,
                   a.max_pages, (int)a.q_len, (int)a.n_heads, (int)a.n_kv_heads, group,
                   (int)a.page_size, (int)(a.q_len * group), make_div((uint32_t)a.page_size),
                   make_div((uint32_t)group), a.scale * LOG2E, a.causal ? 1 : 0,
-                  (int)(a.window < 0x7FFFFFFF ? a.window : 0x7FFFFFFF), (int)a.n_seqs,
-                  p.row_tiles, p.tile_rows, p.target, p.split, a.out, a.lse, ml,
-                  p.split ? ml + p.units * p.tile_rows * 2 : nullptr};
+                  (int)window, (int)a.n_seqs, p.row_tiles, p.tile_rows, p.target, p.split, a.out,
+                  a.lse, ml, p.split ? ml + p.units * p.tile_rows * 2 : nullptr};
     const int64_t wgs = p.units;
     if (p.rt == 0)
         hipLaunchKernelGGL(nvfp4_attention_wide_kernel<64>, dim3((unsigned)wgs),

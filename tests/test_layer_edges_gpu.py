@@ -9,7 +9,7 @@ import nvfp4_block_scaled_amax_amd as mxq
 from nvfp4_block_scaled_amax_amd import api
 from nvfp4_block_scaled_amax_amd import workloads as W
 from gpu_util import announce, dev, require_gpu
-from test_layer_gpu import attention_case, bf16, put
+from test_layer_gpu import attention_case, bf16, check_attention, put, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,25 @@ def test_a_disabled_expert_stays_in_the_softmax(T, E, k, dtype):
     assert (np.abs(got - w) <= w * 2.0 ** -20).all()
     # The function whose gradient moe_route_backward gives.
     assert np.array_equal(w, R.route_weights(x, want, mxq.MXQ_SCORE_SOFTMAX, False, 1.0))
+
+
+# ---------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens,Q,H,Hkv,D,page", [
+    ([3, 0, 1, 40], 6, 4, 2, 128, 16), ([5, 2], 40, 2, 1, 256, 16),
+    ([150, 3, 260], 200, 16, 16, 64, 16),                # the kernel for many rows
+    ([1500], 1, 8, 2, 64, 32), ([700, 9], 30, 4, 1, 128, 48),
+])
+def test_attention_window_past_every_key(lens, Q, H, Hkv, D, page):
+    """However wide, a window that holds all keys is none, also for queries that
+    stand before the first key."""
+    rng = np.random.default_rng(sum(lens) + Q)
+    case = attention_case(rng, lens, Q, H, Hkv, D, page)
+    want = check_attention(case, Hkv, page, "no window")
+    for window in (max(lens) + Q, (1 << 30) + 5, (1 << 31) - 2, (1 << 31) - 1, 1 << 31, 1 << 62,
+                   (1 << 63) - 1):
+        got = run_attention(*case, Hkv, page, None, True, window)
+        torch.cuda.synchronize()
+        assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse), window
