@@ -71,6 +71,8 @@ constexpr float TOP = 11.0f, SLACK = 4.0f;          // numerators: 2^TOP at m, 2
 constexpr float LOW_LOG2 = -14.0f, LOW = 0x1p-14f;  // smaller ones go to further rounds,
 constexpr float LOW_UP = 0x1p29f;                   // each under this factor more
 constexpr float MIN_VS = 0x1p-100f;                 // value scales below count as 0
+constexpr float ZERO_VS = 0x1p-8f;                  // the scale of a tile without other ones
+constexpr float MAX_SUM = 0x1p90f, SUM_STEP = 40.0f;  // a larger sum raises m by this much
 constexpr int ATT_STAGES = 2;                      // tiles in LDS per wavefront
 
 struct AttnK {
@@ -434,7 +436,10 @@ struct ValuePairs {
 // lv = log2 s_v, rv = 2^-lv of the lane group's eight values, whose block scales are
 // vb.  A value scale of 0 (below MIN_VS) stands for a row of zeros, and slots past
 // the length may hold anything: their block scales count as 0, and they take
-// part in the sum under the largest scale beside them.
+// part in the sum under the largest scale of the tile.  In a tile of zeros that is
+// ZERO_VS, about the scale of values of 1, within FP32's range of every other: m
+// follows it, and a sum that began under 2^-100 would overflow at 2^17 keys or
+// vanish beside scales above 2^26.
 template <bool MASKED>
 __device__ __forceinline__ void value_scales(const f32x4_t (&vs)[2], uint32_t (&vb)[8],
                                              float (&lv)[8], float (&rv)[8], int t0, int len,
@@ -447,7 +452,7 @@ __device__ __forceinline__ void value_scales(const f32x4_t (&vs)[2], uint32_t (&
         vmin = __builtin_fminf(vmin, lv[j]);
     }
     if (MASKED || __builtin_amdgcn_ballot_w64(vmin < MIN_VS) != 0) {
-        float vz = MIN_VS;
+        float vz = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const bool live = lv[j] >= MIN_VS && t0 + 16 * (j >> 2) + 4 * g + (j & 3) < len;
@@ -455,6 +460,8 @@ __device__ __forceinline__ void value_scales(const f32x4_t (&vs)[2], uint32_t (&
             lv[j] = live ? lv[j] : 0.0f;
             vz = __builtin_fmaxf(vz, lv[j]);
         }
+        vz = max4_groups(vz);
+        vz = vz > 0.0f ? vz : ZERO_VS;
 #pragma unroll
         for (int j = 0; j < 8; j++)
             lv[j] = lv[j] > 0.0f ? lv[j] : vz;
@@ -492,10 +499,13 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, const f32x4_t (&s)[2][RT]
             zx = __builtin_fmaxf(zx, z[j]);
         }
         // m follows the maximum only when that is past m + SLACK: with m exact, nearly
-        // every step of a short chunk had some row whose maximum rose.
+        // every step of a short chunk had some row whose maximum rose.  It also rises
+        // where the sum, whose terms are up to 2^(TOP + SLACK) / s_v, nears FP32's range.
         zx = max4_groups(zx);
-        if (__builtin_amdgcn_ballot_w64(zx > st.m[rt] + SLACK) != 0) {
-            const float mn = zx > st.m[rt] + SLACK ? zx : st.m[rt];
+        if (__builtin_amdgcn_ballot_w64(zx > st.m[rt] + SLACK || st.l[rt] > MAX_SUM) != 0) {
+            float mn = zx > st.m[rt] + SLACK ? zx : st.m[rt];
+            if (max4_groups(st.l[rt]) > MAX_SUM)
+                mn = __builtin_fmaxf(mn, st.m[rt] + SUM_STEP);
             const float al = __builtin_amdgcn_exp2f(st.m[rt] - mn);
             st.m[rt] = mn;
             st.l[rt] *= al;

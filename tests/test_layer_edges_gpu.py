@@ -110,3 +110,44 @@ def test_attention_window_past_every_key(lens, Q, H, Hkv, D, page):
         got = run_attention(*case, Hkv, page, None, True, window)
         torch.cuda.synchronize()
         assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse), window
+
+
+@pytest.mark.parametrize("n,Q,H,Hkv,D,page", [
+    (140000, 1, 4, 1, 128, 64), (140001, 1, 2, 1, 64, 128), (150000, 2, 1, 1, 256, 16),
+    (140000, 100, 64, 1, 64, 64),                        # the kernel for many rows
+    (33000, 5, 40, 8, 128, 64),
+])
+@pytest.mark.parametrize("values", ["none", "last", "tiny", "huge"])
+def test_attention_sum_over_many_keys_of_small_or_no_values(n, Q, H, Hkv, D, page, values):
+    """Equal scores: lse is the log of the number of keys seen and out the values' mean,
+    also where values are zeros (all of them, or all but the last thousand) or have scales
+    at either end of their range."""
+    announce(f"attention sums n={n} Q={Q} H={H} D={D} {values}")
+    rng = np.random.default_rng(n + D)
+    pages = -(-n // page)
+    rows = pages * Hkv * page
+    k = (np.zeros((rows, D // 2), np.uint8), np.zeros((rows, D // 16), np.uint8),
+         np.zeros(rows, np.float32))
+    codes, blocks, _ = R.random_nvfp4(rng, 1024, D)
+    at = np.arange(rows) % 1021
+    v = [codes[at], blocks[at], np.zeros(rows, np.float32)]
+    t = (np.arange(rows) // (page * Hkv)) * page + np.arange(rows) % page
+    scale = {"none": 0.0, "last": 2.0 ** -10, "tiny": 2.0 ** -100, "huge": 2.0 ** 100}[values]
+    v[2][(t >= n - 1000) | (values == "tiny")] = scale
+    q = bf16(rng.normal(0, 1, (1, Q, H, D)))
+    r = run_attention(q, k, v, np.arange(pages)[None], np.array([n]), Hkv, page, None, True, 0)
+    torch.cuda.synchronize()
+    seen = n - Q + 1 + np.arange(Q)
+    terms = (seen.max() / 16 + 64) * 2.0 ** -23          # one rounding per 16 keys and join
+    lse = r.lse.cpu().double().numpy()[0]
+    assert np.isfinite(lse).all()
+    assert (np.abs(lse - np.log(seen)[:, None]) <= terms + 2.0 ** -17).all()
+    got = r.out.cpu().double().numpy()[0].reshape(Q, Hkv, H // Hkv, D)
+    table = R.decode(codes, blocks)
+    for h in range(Hkv):
+        sel = (np.arange(n) // page * Hkv + h) * page + np.arange(n) % page
+        vals = table[at[sel]] * v[2][sel, None].astype(np.float64)
+        total, mag = np.cumsum(vals, 0)[seen - 1], np.cumsum(np.abs(vals), 0)[seen - 1]
+        want, mag = total / seen[:, None], mag / seen[:, None]
+        tol = mag * (R.HALF_FP16 + 2 * terms) + np.abs(want) * R.HALF_BF16 * 1.001
+        assert (np.abs(got[:, h] - want[:, None]) <= tol[:, None]).all(), h
