@@ -267,6 +267,23 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V],
     return sure;
 }
 
+// A choice's part of the sum of the selected scores, x its logit.  It depends on
+// the scores' ratios alone: a softmax over the selected logits, or sigmoids
+// scaled by e^-h where the largest selected logit, h, is negative, so that no
+// sum underflows.
+template <int L>
+__device__ __forceinline__ float share_of(bool sigmoid, bool mine, float x)
+{
+    float h = over_lanes<L>(mine ? x : -__builtin_inff(), MaxOf{}), w = 0.0f;
+    h = sigmoid && h > 0.0f ? 0.0f : h;
+    if (mine)
+        w = !sigmoid ? exp_f32(x - h)
+            : x >= 0.0f ? 1.0f / (1.0f + exp_f32(-x))
+                        : exp_f32(x - h) / (1.0f + exp_f32(x));
+    const float s = over_lanes<L>(w, SumOf{});
+    return s > 0.0f ? w / s : 0.0f;
+}
+
 __device__ __forceinline__ int popc(uint64_t v) { return __builtin_popcountll(v); }
 
 // Inclusive sum over the 64 lanes: shifts within rows of 16, then the last lane
@@ -376,22 +393,12 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(RouteArgs a)
                 (void)choose<false, L, V, double>(a, x, bias, l, keys + slot * L * V, &chosen,
                                                   &top64, &den64);
             }
-        // Weights.  Renormalized ones depend on the scores' ratios alone: a softmax over
-        // the selected logits, or sigmoids scaled by e^-top where the largest selected
-        // logit, top, is negative, so that no sum underflows.
         const bool mine = l < a.top_k && chosen >= 0;
         float xv = mine ? ld_elem<BF16>(a.logits, t * E + chosen) : -__builtin_inff();
         xv = xv < 3.402823466e+38f ? xv : 3.402823466e+38f;
         float w = 0.0f;
         if (a.renorm) {
-            float h = over_lanes<L>(xv, MaxOf{});
-            h = a.sigmoid && h > 0.0f ? 0.0f : h;
-            if (mine)
-                w = !a.sigmoid ? exp_f32(xv - h)
-                    : xv >= 0.0f ? 1.0f / (1.0f + exp_f32(-xv))
-                                 : exp_f32(xv - h) / (1.0f + exp_f32(xv));
-            const float s = over_lanes<L>(w, SumOf{});
-            w = s > 0.0f ? w / s : 0.0f;
+            w = share_of<L>(a.sigmoid, mine, xv);
         } else if (mine) {
             w = a.sigmoid ? 1.0f / (1.0f + exp_f32(-xv)) : exp_f32(xv - top) / den;
         }
@@ -578,12 +585,14 @@ hipError_t launch_moe_route(bool bf16, const void *logits, const float *bias, in
 }
 
 // ---------------------------------------------------------------------------
-// Router gradient.  With s the scores, S the sum of the selected ones and
-// g_i = scale dw_i: renormalized ds_i = sum_j (g_i - g_j) s_j / S^2 (the form
-// in which equal g_i, and a single choice, give exactly 0), otherwise ds_i =
-// g_i; then dx_e = s_e (1 - s_e) ds_e (sigmoid) or s_e (ds_e - sum_j ds_j
-// s_j) (softmax; the sum is 0 for renormalized weights), ds_e = 0 for
-// unselected experts.  One read of the logits, one write of the gradient.
+// Router gradient.  With s the scores and g_i = scale dw_i:
+//   renormalized, w_i = s_i / sum of the selected s (as the forward forms it, from
+//     the scores' ratios): dx_i = w_i sum_j (g_i - g_j) w_j, times 1 - s_i for
+//     sigmoids (the form in which equal g_i, and a single choice, give exactly 0);
+//   sigmoid: dx_i = g_i s_i (1 - s_i);
+//   softmax: dx_e = s_e (ds_e - sum_j g_j s_j), ds_e = g_e, 0 for unselected experts.
+// Only the last needs the logits of the experts that were not selected.  One
+// read of the logits, one write of the gradient.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -609,70 +618,73 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(Route
     const int E = a.n_experts;
     constexpr float LOW = -3.402823466e+38f;
     auto score_in = [&](float f) { return f < -LOW ? f : -LOW; };
-    float s[V], m = LOW;
-    bool dead[V];
-#pragma unroll
-    for (int j = 0; j < V; j++) {
-        const int e = L * j + l;
-        const float f = e < E ? ld_elem<BF16>(a.logits, tt * E + e) : -__builtin_inff();
-        dead[j] = is_masked(f);
-        s[j] = dead[j] ? LOW : score_in(f);
-        m = s[j] > m ? s[j] : m;
-    }
     // Choice l of the token: its expert, gradient and logit.
-    int64_t e64 = l < a.top_k ? a.experts[tt * a.top_k + l] : -1;
-    const int ce = e64 >= 0 && e64 < E ? (int)e64 : -1;
+    const int64_t e64 = l < a.top_k ? a.experts[tt * a.top_k + l] : -1;
+    int ce = e64 >= 0 && e64 < E ? (int)e64 : -1;
+    float cx = ce >= 0 ? ld_elem<BF16>(a.logits, tt * E + ce) : LOW;
+    ce = is_masked(cx) ? -1 : ce;
+    cx = score_in(cx);
     const float cg = ce >= 0 ? a.d_weights[tt * a.top_k + l] * a.scale : 0.0f;
-    float cx = ce >= 0 ? ld_elem<BF16>(a.logits, tt * E + ce) : -__builtin_inff();
-    const bool cdead = is_masked(cx);
-    cx = cdead ? LOW : score_in(cx);
-    float r = 1.0f;
-    if (!a.sigmoid) {
-        m = over_lanes<L>(m, MaxOf{});
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; j++) {
-            s[j] = dead[j] ? 0.0f : exp_f32(s[j] - m);
-            sum += s[j];
-        }
-        sum = over_lanes<L>(sum, SumOf{});
-        r = sum > 0.0f ? 1.0f / sum : 0.0f;
-    }
-    auto sigmoid = [](float v) { return 1.0f / (1.0f + exp_f32(-v)); };
-#pragma unroll
-    for (int j = 0; j < V; j++)
-        s[j] = a.sigmoid ? (dead[j] ? 0.0f : sigmoid(s[j])) : s[j] * r;
-    const float cs = cdead ? 0.0f : a.sigmoid ? sigmoid(cx) : exp_f32(cx - m) * r;
-    // ds of every choice, then to the experts' lanes.
+    const float cs = 1.0f / (1.0f + exp_f32(-cx));                   // sigmoid
     const uint32_t lane0 = lane_id() & ~(uint32_t)(L - 1);
-    float S = 0.0f, cd = cg, gs = 0.0f;
-    if (a.renorm) {
-        cd = 0.0f;
-        for (int c = 0; c < a.top_k; c++) {
-            const float sc = lane_get(cs, lane0 + c), gc = lane_get(cg, lane0 + c);
-            S += sc;
-            cd = __builtin_fmaf(cg - gc, sc, cd);
+    float d[V] = {}, cd;
+    if (!a.renorm && a.sigmoid) {
+        cd = cg * cs * (1.0f - cs);
+    } else {
+        float q, s[V];
+        if (a.renorm) {
+            q = share_of<L>(a.sigmoid, ce >= 0, cx);
+        } else {
+            float m = LOW, sum = 0.0f;
+            bool dead[V];
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                const int e = L * j + l;
+                const float f = e < E ? ld_elem<BF16>(a.logits, tt * E + e) : -__builtin_inff();
+                dead[j] = is_masked(f);
+                s[j] = dead[j] ? LOW : score_in(f);
+                m = s[j] > m ? s[j] : m;
+            }
+            m = over_lanes<L>(m, MaxOf{});
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                s[j] = dead[j] ? 0.0f : exp_f32(s[j] - m);
+                sum += s[j];
+            }
+            sum = over_lanes<L>(sum, SumOf{});
+            const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; j++)
+                s[j] *= r;
+            q = ce >= 0 ? exp_f32(cx - m) * r : 0.0f;
         }
-        const float q = S > 0.0f ? 1.0f / S : 0.0f;
-        cd = ce >= 0 ? cd * q * q : 0.0f;
-    } else if (!a.sigmoid) {
-        for (int c = 0; c < a.top_k; c++)
-            gs = __builtin_fmaf(lane_get(cg, lane0 + c), lane_get(cs, lane0 + c), gs);
+        float u = 0.0f, gs = 0.0f;
+        for (int c = 0; c < a.top_k; c++) {
+            const float qc = lane_get(q, lane0 + c), gc = lane_get(cg, lane0 + c);
+            u = __builtin_fmaf(cg - gc, qc, u);
+            gs = __builtin_fmaf(gc, qc, gs);
+        }
+        cd = a.renorm ? q * u : q * cg;
+        if (a.sigmoid)
+            cd *= 1.0f - cs;
+        if (!a.renorm)
+#pragma unroll
+            for (int j = 0; j < V; j++)
+                d[j] = -s[j] * gs;
     }
-    float ds[V] = {};
+    // To the experts' lanes.
     for (int c = 0; c < a.top_k; c++) {
         const int ec = lane_get(ce, lane0 + c);
         const float dc = lane_get(cd, lane0 + c);
 #pragma unroll
         for (int j = 0; j < V; j++)
-            ds[j] += L * j + l == ec ? dc : 0.0f;
+            d[j] += L * j + l == ec ? dc : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < V; j++) {
         const int e = L * j + l;
-        const float d = a.sigmoid ? ds[j] * s[j] * (1.0f - s[j]) : s[j] * (ds[j] - gs);
         if (live && e < E)
-            st_elem<BF16>(a.d_logits, t * E + e, d);
+            st_elem<BF16>(a.d_logits, t * E + e, d[j]);
     }
 }
 

@@ -151,3 +151,72 @@ def test_attention_sum_over_many_keys_of_small_or_no_values(n, Q, H, Hkv, D, pag
         want, mag = total / seen[:, None], mag / seen[:, None]
         tol = mag * (R.HALF_FP16 + 2 * terms) + np.abs(want) * R.HALF_BF16 * 1.001
         assert (np.abs(got[:, h] - want[:, None]) <= tol[:, None]).all(), h
+
+
+# ---------------------------------------------------------------------------
+# The router's gradient where scores are near 0 or 1
+# ---------------------------------------------------------------------------
+
+def log_sigmoid(x):
+    return -np.logaddexp(0.0, -x)
+
+
+def renormalized_gradient(dw, x, experts, scoring):
+    """d_logits of weights s_i / sum of the selected s, from the logarithms of the
+    scores, and the sum of its terms' magnitudes."""
+    live = experts >= 0
+    xc = np.where(live, np.take_along_axis(x, np.maximum(experts, 0), 1), -np.inf)
+    ls = np.where(live, log_sigmoid(np.where(live, xc, 0.0)) if scoring else xc, -np.inf)
+    top = ls.max(1, keepdims=True)
+    w = np.exp(ls - np.where(top > -np.inf, top, 0.0))
+    w /= np.maximum(w.sum(1, keepdims=True), 1e-300)
+    g = np.where(live, dw, 0.0)
+    diff = g[:, :, None] - g[:, None, :]
+    down = np.exp(log_sigmoid(-np.where(live, xc, 0.0))) if scoring else 1.0
+    out, mag = np.zeros_like(x), np.zeros_like(x)
+    for a, d in ((out, diff), (mag, np.abs(diff))):
+        v = w * (d * w[:, None, :]).sum(2) * down
+        t, c = np.nonzero(live)
+        a[t, experts[t, c]] = v[t, c]
+    return out, mag
+
+
+def check_gradient(x, experts, dw, scoring, renorm, want, mag, name):
+    """Scores within 2^-19, one rounding of each term and sum, at most 20 terms."""
+    announce(f"gradient {name} {x.shape}")
+    d = api.moe_route_backward(put(dw, torch.float32), put(x, torch.float32),
+                               put(experts, torch.int64), scoring, renorm)
+    torch.cuda.synchronize()
+    got = d.cpu().double().numpy()
+    bad = np.argwhere(~(np.abs(got - want) <= mag * (2.0 ** -17 + 25 * 2.0 ** -24) + 1e-37))
+    assert bad.size == 0, (name, len(bad), tuple(bad[0]), got[tuple(bad[0])], want[tuple(bad[0])])
+
+
+SMALL = {
+    "sigmoids of -95": (mxq.MXQ_SCORE_SIGMOID, -95.0, 4.0),
+    "sigmoids of -1000": (mxq.MXQ_SCORE_SIGMOID, -1000.0, 4.0),
+    "softmax 100 below the largest": (mxq.MXQ_SCORE_SOFTMAX, -100.0, 3.0),
+    "softmax 1e4 below the largest": (mxq.MXQ_SCORE_SOFTMAX, -1e4, 3.0),
+}
+
+
+@pytest.mark.parametrize("name", SMALL)
+@pytest.mark.parametrize("T,E,k", [(33, 20, 6), (9, 300, 20)])
+def test_gradient_of_renormalized_small_scores(T, E, k, name):
+    """The weights depend on the scores' ratios alone, and so does their gradient,
+    however small the selected scores: with an expert disabled that has nearly all
+    of the softmax, or sigmoids below FP32's range."""
+    scoring, at, spread = SMALL[name]
+    rng = np.random.default_rng(E)
+    x = rng.normal(at, spread, (T, E)).astype(np.float32).astype(np.float64)
+    x[:, 3] = 2.0                                        # disabled by the bias
+    x[0, 5:] = -np.inf
+    b = np.zeros(E, np.float32)
+    b[3] = -np.inf
+    xt = put(x, torch.float32)
+    r = api.moe_route(xt, k, bias=put(b, torch.float32), scoring=scoring, scale=1.0)
+    experts = r.experts.cpu().numpy()
+    assert not (experts == 3).any()
+    dw = rng.normal(0, 1, (T, k)).astype(np.float32).astype(np.float64)
+    want, mag = renormalized_gradient(dw, x, experts, scoring)
+    check_gradient(x, experts, dw, scoring, True, want, mag, name)
