@@ -585,12 +585,14 @@ hipError_t launch_moe_route(bool bf16, const void *logits, const float *bias, in
 }
 
 // ---------------------------------------------------------------------------
-// Router gradient.  With s the scores and g_i = scale dw_i:
-//   renormalized, w_i = s_i / sum of the selected s (as the forward forms it, from
-//     the scores' ratios): dx_i = w_i sum_j (g_i - g_j) w_j, times 1 - s_i for
-//     sigmoids (the form in which equal g_i, and a single choice, give exactly 0);
-//   sigmoid: dx_i = g_i s_i (1 - s_i);
-//   softmax: dx_e = s_e (ds_e - sum_j g_j s_j), ds_e = g_e, 0 for unselected experts.
+// Router gradient.  With s the scores and g_i = scale dw_i, in forms that lose
+// nothing where scores are near 0 or 1, and in which equal g_i of renormalized
+// weights, and a single choice, give exactly 0:
+//   renormalized, w_i = s_i / sum of the selected s (as the forward forms it):
+//     dx_i = w_i sum_j (g_i - g_j) w_j, times 1 - s_i = sigmoid(-x_i) for sigmoids;
+//   sigmoid: dx_i = g_i s_i (1 - s_i), s (1 - s) = e / (1 + e)^2 with e = e^-|x|;
+//   softmax: dx_i = s_i (sum_j (g_i - g_j) s_j + g_i U) for a selected i, U the sum
+//     of the other experts' scores, and -s_e sum_j g_j s_j for the others.
 // Only the last needs the logits of the experts that were not selected.  One
 // read of the logits, one write of the gradient.
 // ---------------------------------------------------------------------------
@@ -625,13 +627,13 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(Route
     ce = is_masked(cx) ? -1 : ce;
     cx = score_in(cx);
     const float cg = ce >= 0 ? a.d_weights[tt * a.top_k + l] * a.scale : 0.0f;
-    const float cs = 1.0f / (1.0f + exp_f32(-cx));                   // sigmoid
+    const float ce_abs = exp_f32(cx < 0.0f ? cx : -cx);              // e^-|x|
     const uint32_t lane0 = lane_id() & ~(uint32_t)(L - 1);
     float d[V] = {}, cd;
     if (!a.renorm && a.sigmoid) {
-        cd = cg * cs * (1.0f - cs);
+        cd = cg * ce_abs / ((1.0f + ce_abs) * (1.0f + ce_abs));
     } else {
-        float q, s[V];
+        float q, others = 0.0f, s[V];
         if (a.renorm) {
             q = share_of<L>(a.sigmoid, ce >= 0, cx);
         } else {
@@ -646,27 +648,35 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(Route
                 m = s[j] > m ? s[j] : m;
             }
             m = over_lanes<L>(m, MaxOf{});
+            uint32_t selected = 0;                // of the lane's experts
+            for (int c = 0; c < a.top_k; c++) {
+                const int ec = lane_get(ce, lane0 + c);
+                selected |= ec >= 0 && (ec & (L - 1)) == l ? 1u << (ec / L) : 0u;
+            }
 #pragma unroll
             for (int j = 0; j < V; j++) {
                 s[j] = dead[j] ? 0.0f : exp_f32(s[j] - m);
                 sum += s[j];
+                s[j] = (selected >> j) & 1 ? 0.0f : s[j];
+                others += s[j];
             }
             sum = over_lanes<L>(sum, SumOf{});
             const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+            others = over_lanes<L>(others, SumOf{}) * r;
 #pragma unroll
             for (int j = 0; j < V; j++)
                 s[j] *= r;
             q = ce >= 0 ? exp_f32(cx - m) * r : 0.0f;
         }
-        float u = 0.0f, gs = 0.0f;
+        float u = cg * others, gs = 0.0f;
         for (int c = 0; c < a.top_k; c++) {
             const float qc = lane_get(q, lane0 + c), gc = lane_get(cg, lane0 + c);
             u = __builtin_fmaf(cg - gc, qc, u);
             gs = __builtin_fmaf(gc, qc, gs);
         }
-        cd = a.renorm ? q * u : q * cg;
+        cd = q * u;
         if (a.sigmoid)
-            cd *= 1.0f - cs;
+            cd *= (cx < 0.0f ? 1.0f : ce_abs) / (1.0f + ce_abs);
         if (!a.renorm)
 #pragma unroll
             for (int j = 0; j < V; j++)

@@ -195,6 +195,8 @@ def check_gradient(x, experts, dw, scoring, renorm, want, mag, name):
 SMALL = {
     "sigmoids of -95": (mxq.MXQ_SCORE_SIGMOID, -95.0, 4.0),
     "sigmoids of -1000": (mxq.MXQ_SCORE_SIGMOID, -1000.0, 4.0),
+    "sigmoids about 0": (mxq.MXQ_SCORE_SIGMOID, 0.0, 3.0),
+    "sigmoids of 25": (mxq.MXQ_SCORE_SIGMOID, 25.0, 6.0),
     "softmax 100 below the largest": (mxq.MXQ_SCORE_SOFTMAX, -100.0, 3.0),
     "softmax 1e4 below the largest": (mxq.MXQ_SCORE_SOFTMAX, -1e4, 3.0),
 }
@@ -220,3 +222,32 @@ def test_gradient_of_renormalized_small_scores(T, E, k, name):
     dw = rng.normal(0, 1, (T, k)).astype(np.float32).astype(np.float64)
     want, mag = renormalized_gradient(dw, x, experts, scoring)
     check_gradient(x, experts, dw, scoring, True, want, mag, name)
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 16, 5), (9, 300, 20), (3, 1024, 64)])
+def test_gradient_of_scores_near_one(T, E, k):
+    """Sigmoids to either side of 1 - 2^-24, and a softmax that one selected expert
+    has nearly all of: 1 - s is what the gradient is made of."""
+    rng = np.random.default_rng(T + E)
+    experts = np.argsort(rng.random((T, E)), 1)[:, :k]
+    experts[:, -1] = -1
+    dw = rng.normal(0, 1, (T, k)).astype(np.float32).astype(np.float64)
+    g = np.zeros((T, E))
+    np.put_along_axis(g, experts[:, :-1], dw[:, :-1], 1)
+
+    x = rng.uniform(-30, 60, (T, E)).astype(np.float32).astype(np.float64)
+    want = g * np.exp(log_sigmoid(x) + log_sigmoid(-x))
+    check_gradient(x, experts, dw, mxq.MXQ_SCORE_SIGMOID, False, want, np.abs(want), "sigmoids")
+
+    # The first choice has all but about e^-a of the softmax.
+    x = rng.normal(0, 1, (T, E))
+    np.put_along_axis(x, experts[:, :1], rng.uniform(10, 40, (T, 1)), 1)
+    x = x.astype(np.float32).astype(np.float64)
+    s = np.exp(x - x.max(1, keepdims=True))
+    s /= s.sum(1, keepdims=True)
+    selected = np.zeros((T, E), bool)
+    np.put_along_axis(selected, experts[:, :-1], True, 1)
+    # sum_j ds_j s_j over all experts: dx_e = s_e sum_j (ds_e - ds_j) s_j, term by term.
+    diff = g[:, :, None] - g[:, None, :]
+    want, mag = (s * (d * s[:, None, :]).sum(2) for d in (diff, np.abs(diff)))
+    check_gradient(x, experts, dw, mxq.MXQ_SCORE_SOFTMAX, False, want, mag, "softmax")
