@@ -9,7 +9,8 @@ import nvfp4_block_scaled_amax_amd as mxq
 from nvfp4_block_scaled_amax_amd import api
 from nvfp4_block_scaled_amax_amd import workloads as W
 from gpu_util import announce, dev, require_gpu
-from test_layer_gpu import attention_case, bf16, check_attention, put, run_attention
+from test_layer_gpu import (X_KINDS, activation, attention_case, bf16, check_attention, close, product,
+                            put, run_attention, segments)
 
 pytestmark = pytest.mark.gpu
 
@@ -251,3 +252,121 @@ def test_gradient_of_scores_near_one(T, E, k):
     diff = g[:, :, None] - g[:, None, :]
     want, mag = (s * (d * s[:, None, :]).sum(2) for d in (diff, np.abs(diff)))
     check_gradient(x, experts, dw, mxq.MXQ_SCORE_SOFTMAX, False, want, mag, "softmax")
+
+
+# ---------------------------------------------------------------------------
+# Few-row products of many weights: wavefronts that take whole tiles of 16
+# weight rows, from 2048 tiles on
+# ---------------------------------------------------------------------------
+
+def tiles(n):
+    return -(-n // 16)
+
+
+@pytest.mark.parametrize("kind", X_KINDS)
+@pytest.mark.parametrize("M,N,K", [
+    (1, 32777, 64), (13, 32790, 192), (16, 32768, 128), (17, 33001, 320), (64, 32801, 704),
+    (33, 40007, 576), (1, 65551, 448), (24, 32769, 2112), (17, 32785, 2048), (5, 32783, 6208),
+])
+def test_matvec_of_many_weights(M, N, K, kind):
+    """Ends of K inside a unit of 128 and a block of 512, of N inside a tile and a round
+    of the wavefronts; one and two groups of 16 rows, one and several passes."""
+    assert tiles(N) >= 2048
+    announce(f"matvec {M}x{N}x{K} {kind}")
+    rng = np.random.default_rng(M + N + K)
+    x, xv, sx, held = activation(rng, M, K, kind)
+    c, b, _ = R.random_nvfp4(rng, N, K)
+    c[-1], b[-1] = c[0], b[0]
+    w = R.decode(c, b)
+    for rpb, out in ((N, torch.bfloat16), (16, torch.float32)):
+        s = np.exp2(rng.uniform(-9, -3, -(-N // rpb))).astype(np.float32)
+        want, tol = product(xv, sx, w, np.repeat(s, rpb)[:N].astype(np.float64), held)
+        got = api.nvfp4_matvec(x, dev(c), dev(b), dev(s), rpb, out)
+        torch.cuda.synchronize()
+        close(got, want, tol + (np.abs(want) * R.HALF_BF16 * 1.001
+                                if out == torch.bfloat16 else 0), f"matvec {rpb} {out}")
+
+
+@pytest.mark.parametrize("kind", X_KINDS)
+@pytest.mark.parametrize("G,rows,N,K", [
+    (128, 200, 257, 192), (70, 90, 480, 320), (64, 300, 1000, 704), (40, 41, 830, 64),
+    (16, 600, 2050, 128), (130, 1000, 250, 64), (24, 50, 1370, 1088),
+])
+def test_experts_of_many_weights(G, rows, N, K, kind):
+    """The same per expert, alone and as the gated pair, with segments larger than the
+    rows staged at once."""
+    assert min(G, rows) * tiles(N) >= 2048
+    announce(f"experts {G} {rows}x{N}x{K} {kind}")
+    rng = np.random.default_rng(G + rows + N)
+    seg = segments(rng, G, rows)
+    T = max(1, rows // 3)
+    rt = rng.integers(0, T, rows)
+    rt[0] = -1
+    x, xv, sx, held = activation(rng, rows, K, kind)
+    xt, xtv, sxt, _ = activation(rng, T, K, kind)
+    (gc, gb, s), (uc, ub, _) = (R.random_nvfp4(rng, G * N, K) for _ in range(2))
+    s = (s[:G] * 2.0 ** -6).astype(np.float32)
+    gd, gbd, ud, ubd = (dev(a.reshape(G, N, -1)) for a in (gc, gb, uc, ub))
+    got = torch.full((rows, N), 5.0, device="cuda")
+    args = (x.codes, x.block_scales, x.fp32_scales) if kind == "nvfp4" else (x, None, None)
+    mxq.mxq_nvfp4_expert_matvec(X_KINDS.index(kind), *args, gd, gbd, dev(s), dev(seg), G, rows, N,
+                                K, mxq.MXQ_OUT_F32, got)
+    h = api.nvfp4_expert_gateup(xt, api.GateUpNVFP4(gd, gbd, ud, ubd, dev(s)), dev(rt), dev(seg),
+                                torch.float32)
+    torch.cuda.synchronize()
+    assert (got[seg[-1]:] == 5.0).all()
+    for e in range(G):
+        a, z = seg[e], seg[e + 1]
+        if z == a:
+            continue
+        at = slice(e * N, (e + 1) * N)
+        wg, wu, sc = R.decode(gc[at], gb[at]), R.decode(uc[at], ub[at]), np.full(N, float(s[e]))
+        want, tol = product(xv[a:z], sx[a:z], wg, sc, held)
+        close(got[a:z], want, tol, f"expert {e}")
+        t = np.maximum(rt[a:z], 0)
+        (g, tg), (u, tu) = (product(xtv[t], sxt[t], w, sc, held) for w in (wg, wu))
+        with np.errstate(over="ignore"):
+            silu = g / (1 + np.exp(-g))
+        # |silu'| <= 1.1; silu itself within 2^-20.
+        tol = 1.1 * tg * (np.abs(u) + tu) + np.abs(silu) * tu + np.abs(silu * u) * 2.0 ** -20
+        close(h[a:z], silu * u, tol + 1e-36, f"gated pair of expert {e}")
+
+
+# ---------------------------------------------------------------------------
+# Attention over long walks and large batches
+# ---------------------------------------------------------------------------
+
+def shared_pages_case(rng, lens, Q, H, Hkv, D, page, n_pages):
+    """As attention_case, the sequences' tables drawn from the same few pages."""
+    per = max(1, max(-(-n // page) for n in lens))
+    table = rng.integers(0, n_pages, (len(lens), per))
+    rows = n_pages * Hkv * page
+    k, v = (R.random_nvfp4(rng, rows, D, zero_rows=0.05) for _ in "kv")
+    q = bf16(rng.normal(0, 1, (len(lens), Q, H, D)) * 0.25)
+    return q, k, v, table, np.array(lens, np.int64)
+
+
+@pytest.mark.parametrize("lens,Q,H,Hkv,D,page,causal,window", [
+    ([17000] + [40, 0, 300] * 53, 1, 8, 4, 64, 16, True, 0),
+    ([9000, 8200] + [7] * 159, 1, 4, 4, 128, 48, True, 8500),
+    ([8500] + [33] * 29, 33, 16, 16, 64, 16, True, 0),   # the kernel for many rows
+    ([100] * 15 + [17000] + [64] * 14, 33, 16, 16, 64, 64, False, 0),
+])
+def test_attention_walks_past_a_window_of_pages(lens, Q, H, Hkv, D, page, causal, window):
+    """One workgroup per sequence and head, whose wavefronts look pages up 64 tiles at a
+    time: sequences of 8192 keys and more need a second look-up, and a third."""
+    rng = np.random.default_rng(max(lens) + D)
+    check_attention(shared_pages_case(rng, lens, Q, H, Hkv, D, page, 200), Hkv, page, "long walk",
+                    causal=causal, window=window)
+
+
+@pytest.mark.parametrize("B,Q,H,Hkv,D", [(65, 1, 4, 2, 128), (130, 1, 6, 1, 64), (200, 3, 2, 1, 256),
+                                         (70, 40, 3, 3, 64)])
+def test_attention_parts_of_more_than_64_sequences(B, Q, H, Hkv, D):
+    """The plan's prefix sums over the sequences in more than one round, with empty
+    sequences and long ones in every round."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in np.exp2(rng.uniform(0, 11, B))]
+    lens[3] = lens[B - 1] = 0
+    lens[64] = 4000
+    check_attention(shared_pages_case(rng, lens, Q, H, Hkv, D, 32, 300), Hkv, 32, "large batch")
