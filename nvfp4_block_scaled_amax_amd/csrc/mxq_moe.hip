@@ -180,7 +180,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V],
                          (T)bias[j];
     }
     bool sure = true;
-    auto close_keys = [&](T hi, T lo) {
+    auto close_keys = [&](T hi, T lo, T doubt) {
         const T size = hi > -lo ? hi : -lo;
         return sizeof(T) == 4 && !by_logit && lo != none<T>() &&
                hi - lo <= doubt + (T)0x1p-20 * (size > (T)0 ? size : (T)0);
@@ -191,7 +191,9 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V],
         for (int j = 0; j < V; j++)
             lds[l * V + j] = key[j];
         constexpr int GS = 64 / L;
-        T gs[GS];
+        // A sum of two keys is as uncertain as the keys are large, however small it is
+        // itself (size: the most of any group).
+        T gs[GS], size = 0;
 #pragma unroll
         for (int i = 0; i < GS; i++) {
             const int g = l + L * i;
@@ -212,8 +214,15 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V],
                         m2 = lo > m2 ? lo : m2;
                     }
                 }
-            gs[i] = a.group_topk == 2 && m2 != none<T>() ? m1 + m2 : m1;
+            const bool two = a.group_topk == 2 && m2 != none<T>();
+            gs[i] = two ? m1 + m2 : m1;
+            const T sz = (m1 < 0 ? -m1 : m1) + (m2 < 0 ? -m2 : m2);
+            size = two && sz > size ? sz : size;
         }
+        T group_doubt = doubt;
+        if constexpr (sizeof(T) == 4 && !by_logit)
+            if (a.group_topk == 2)
+                group_doubt = 2 * doubt + (T)0x1p-20 * over_lanes<L>(size, MaxOf{});
         uint64_t keep = 0;
         T last = none<T>();
         for (int r = 0; r <= a.topk_groups; r++) {
@@ -223,7 +232,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V],
                 v = gs[i] > v ? gs[i] : v;
             v = over_lanes<L>(v, MaxOf{});
             if (r == a.topk_groups) {             // the best group left out
-                sure = sure && !close_keys(last, v);
+                sure = sure && !close_keys(last, v, group_doubt);
                 break;
             }
             int g = 1 << 20;
@@ -253,7 +262,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V],
         int i;
         const T v = best_key<L, V, T>(key, l, &i);
         if (c > 0)
-            sure = sure && !close_keys(last, v);
+            sure = sure && !close_keys(last, v, doubt);
         if (c == a.top_k)
             break;
         const bool some = v != none<T>();

@@ -9,8 +9,8 @@ import nvfp4_block_scaled_amax_amd as mxq
 from nvfp4_block_scaled_amax_amd import api
 from nvfp4_block_scaled_amax_amd import workloads as W
 from gpu_util import announce, dev, require_gpu
-from test_layer_gpu import (X_KINDS, activation, attention_case, bf16, check_attention, close, product,
-                            put, run_attention, segments)
+from test_layer_gpu import (X_KINDS, activation, attention_case, bf16, check_attention, check_route, close,
+                            params, product, put, run_attention, segments)
 
 pytestmark = pytest.mark.gpu
 
@@ -89,6 +89,23 @@ def test_a_disabled_expert_stays_in_the_softmax(T, E, k, dtype):
     assert (np.abs(got - w) <= w * 2.0 ** -20).all()
     # The function whose gradient moe_route_backward gives.
     assert np.array_equal(w, R.route_weights(x, want, mxq.MXQ_SCORE_SOFTMAX, False, 1.0))
+
+
+@pytest.mark.parametrize("scoring", [mxq.MXQ_SCORE_SOFTMAX, mxq.MXQ_SCORE_SIGMOID])
+@pytest.mark.parametrize("T,E,groups,at", [(32, 128, 64, 1e6), (2000, 128, 64, 4096.0),
+                                           (3000, 96, 32, 300.0), (500, 512, 16, 32768.0)])
+def test_group_sums_of_keys_that_cancel(T, E, groups, at, scoring):
+    """A group's two best keys, large of either sign: their sum is small, but FP32 holds
+    each only to 2^-24 of its size."""
+    announce(f"group sums {T}x{E} {scoring}")
+    rng = np.random.default_rng(T + E)
+    x = rng.normal(0, 1.0, (T, E)).astype(np.float32).astype(np.float64)
+    per = E // groups
+    b = np.where(np.arange(E) % per == 0, at, -at)
+    b[np.arange(E) % per > 1] = -np.inf
+    # Both experts of the best group: only the sums decide.
+    check_route(x, b, params(2, scoring, groups, 1, 2), torch.float32, "group sums")
+    check_route(x, b, params(6, scoring, groups, groups // 4, 2), torch.float32, "group sums")
 
 
 # ---------------------------------------------------------------------------
