@@ -774,8 +774,9 @@ typedef struct {
  *   block_table [n_seqs][max_pages] int64, seq_lens [n_seqs] int64, device data:
  *   lengths are clamped into [0, max_pages * page_size] and pages into
  *   [0, n_pages), so malformed ones give meaningless rows, never an access out
- *   of bounds; entries past a sequence's last page are not read.  Slots past
- *   the length may hold anything.
+ *   of bounds; entries past a sequence's last page are not read.  Slots that
+ *   no query sees (past the length, before the first query's window) may hold
+ *   anything.
  *   softmax_scale > 0; window >= 0, and 0 if not causal (MXQ_ERR_ARG).
  *   workspace: mxq_nvfp4_attention_workspace(...) bytes.
  *   n_seqs * q_len * n_heads <= 2^25, max_pages * page_size <= 2^30, cache rows

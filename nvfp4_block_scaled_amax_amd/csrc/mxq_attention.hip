@@ -434,16 +434,17 @@ struct ValuePairs {
 };
 
 // lv = log2 s_v, rv = 2^-lv of the lane group's eight values, whose block scales are
-// vb.  A value scale of 0 (below MIN_VS) stands for a row of zeros, and slots past
-// the length may hold anything: their block scales count as 0, and they take
+// vb.  A value scale of 0 (below MIN_VS) stands for a row of zeros, and slots that no
+// row of the tile sees (outside keys [klo, khi): past the length, before the
+// window) may hold anything: their block scales count as 0, and they take
 // part in the sum under the largest scale of the tile.  In a tile of zeros that is
 // ZERO_VS, about the scale of values of 1, within FP32's range of every other: m
 // follows it, and a sum that began under 2^-100 would overflow at 2^17 keys or
 // vanish beside scales above 2^26.
 template <bool MASKED>
 __device__ __forceinline__ void value_scales(const f32x4_t (&vs)[2], uint32_t (&vb)[8],
-                                             float (&lv)[8], float (&rv)[8], int t0, int len,
-                                             int g)
+                                             float (&lv)[8], float (&rv)[8], int t0, int klo,
+                                             int khi, int g)
 {
     float vmin = vs[0][0];
 #pragma unroll
@@ -455,7 +456,8 @@ __device__ __forceinline__ void value_scales(const f32x4_t (&vs)[2], uint32_t (&
         float vz = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const bool live = lv[j] >= MIN_VS && t0 + 16 * (j >> 2) + 4 * g + (j & 3) < len;
+            const int t = t0 + 16 * (j >> 2) + 4 * g + (j & 3);
+            const bool live = lv[j] >= MIN_VS && t >= klo && t < khi;
             vb[j] = live ? vb[j] : 0;
             lv[j] = live ? lv[j] : 0.0f;
             vz = __builtin_fmaxf(vz, lv[j]);
@@ -566,7 +568,7 @@ __device__ __forceinline__ void weigh(Rows<D, RT> &st, const f32x4_t (&s)[2][RT]
 
 // One step: the tile at LDS address x (keys t0 ..).
 template <int D, int RT, bool MASKED>
-__device__ __forceinline__ void attend(Rows<D, RT> &st, uint32_t x, int t0, int len,
+__device__ __forceinline__ void attend(Rows<D, RT> &st, uint32_t x, int t0, int klo, int khi,
                                        const int (&lo)[RT], const int (&hi)[RT], int l, int g)
 {
     using St = Stage<D>;
@@ -641,15 +643,15 @@ __device__ __forceinline__ void attend(Rows<D, RT> &st, uint32_t x, int t0, int 
         vb[j] = lds_ld<uint8_t>(pvb + key * (D / 16));
     }
     float lv[8], rv[8];
-    value_scales<MASKED>(vs, vb, lv, rv, t0, len, g);
+    value_scales<MASKED>(vs, vb, lv, rv, t0, klo, khi, g);
     const ValuePairs<VW> v(vc, vb);
     weigh<D, RT, MASKED>(st, s, ks, lv, rv, t0, lo, hi, g, v, [&](int j) { return v.again(j); });
 }
 
-// What rows r0 .. r1 - 1 of a sequence of len keys see: keys [kmin, kmax) at most, of
-// which every row sees [full_lo, full_hi); kmin is a tile's first key.
+// What rows r0 .. r1 - 1 of a sequence of len keys see: keys [klo, kmax) at most, of
+// which every row sees [full_lo, full_hi); kmin is the first key of klo's tile.
 struct Span {
-    int kmin, kmax, full_lo, full_hi;
+    int kmin, klo, kmax, full_lo, full_hi;
 };
 __device__ __forceinline__ Span row_span(const AttnK &a, int r0, int r1, int len)
 {
@@ -657,8 +659,9 @@ __device__ __forceinline__ Span row_span(const AttnK &a, int r0, int r1, int len
     const int last = len - a.q_len + (int)udiv((uint32_t)(r1 - 1), a.group_div);
     Span s;
     s.kmax = a.causal ? (last + 1 < 0 ? 0 : last + 1) : len;
-    const int kmin = a.causal && a.window > 0 ? first - a.window + 1 : 0;
-    s.kmin = kmin < 0 ? 0 : kmin & ~(ATT_TILE - 1);
+    const int klo = a.causal && a.window > 0 ? first - a.window + 1 : 0;
+    s.klo = klo < 0 ? 0 : klo;
+    s.kmin = s.klo & ~(ATT_TILE - 1);
     s.full_hi = a.causal ? (first + 1 < len ? first + 1 : len) : len;
     s.full_lo = a.causal && a.window > 0 ? last - a.window + 1 : 0;
     return s;
@@ -769,8 +772,8 @@ __global__ void __launch_bounds__(ATT_THREADS, D * RT <= 128 ? 3 : 2)
             copy_tile<D>(a, window_rows(win, ahead), mine32 + fill * St::BYTES, lane);
             ahead++;
             wait_copies<(ATT_STAGES - 1) * St::COPIES>();
-            attend<D, RT, decltype(masked)::value>(st, mine32 + buf * St::BYTES, t0, len, lo, hi,
-                                                   l, g);
+            attend<D, RT, decltype(masked)::value>(st, mine32 + buf * St::BYTES, t0, sp.klo,
+                                                   sp.kmax, lo, hi, l, g);
             // The tile has been read before the next step's copies overwrite it.
             asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
             buf = buf == ATT_STAGES - 1 ? 0 : buf + 1;
@@ -924,11 +927,12 @@ struct RawPart {
             *reinterpret_cast<float *>(out + Decoded<D>::KS + 4 * lane) = s[0][0];
     }
     template <bool MASKED>
-    __device__ __forceinline__ void decode_values(uint8_t *out, int t0, int len, int lane)
+    __device__ __forceinline__ void decode_values(uint8_t *out, int t0, int klo, int khi,
+                                                  int lane)
     {
         const int g = lane >> 4;
         float lv[8], rv[8];
-        value_scales<MASKED>(s, b, lv, rv, t0, len, g);
+        value_scales<MASKED>(s, b, lv, rv, t0, klo, khi, g);
         uint32_t codes[8][1];
 #pragma unroll
         for (int j = 0; j < 8; j++)
@@ -1033,7 +1037,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 2) nvfp4_attention_wide_kernel(A
             constexpr bool MASKED = decltype(masked)::value;
             __syncthreads();                         // the last step's tiles have been read
             if (values)
-                raw.template decode_values<MASKED>(out, t + part, len, lane);
+                raw.template decode_values<MASKED>(out, t + part, sp.klo, sp.kmax, lane);
             else
                 raw.decode_keys(out, lane);
             if (ahead == 64) {

@@ -387,3 +387,26 @@ def test_attention_parts_of_more_than_64_sequences(B, Q, H, Hkv, D):
     lens[3] = lens[B - 1] = 0
     lens[64] = 4000
     check_attention(shared_pages_case(rng, lens, Q, H, Hkv, D, 32, 300), Hkv, 32, "large batch")
+
+
+@pytest.mark.parametrize("lens,Q,H,Hkv,D,page,window", [
+    ([200, 77, 34], 1, 8, 2, 128, 16, 20), ([333, 40], 3, 4, 2, 64, 16, 7),
+    ([150], 30, 4, 1, 256, 48, 50), ([500, 260], 100, 32, 32, 64, 32, 33),
+])
+def test_attention_slots_before_the_window_hold_anything(lens, Q, H, Hkv, D, page, window):
+    """Keys that no query sees, in the tile where the window begins, do not reach
+    the result, NaN and infinite scales included."""
+    rng = np.random.default_rng(window)
+    q, k, v, table, lens = case = attention_case(rng, lens, Q, H, Hkv, D, page)
+    want = check_attention(case, Hkv, page, "window", window=window)
+    seen = np.zeros(k[0].shape[0], bool)
+    for b, n in enumerate(lens):
+        t = np.arange(max(0, n - Q - window + 1), n)
+        for h in range(Hkv):
+            seen[(table[b][t // page] * Hkv + h) * page + t % page] = True
+    for bad in (np.nan, np.inf):
+        for c, bs, s in (k, v):
+            c[~seen], bs[~seen], s[~seen] = 0xFF, 0x7F, bad
+        got = run_attention(*case, Hkv, page, None, True, window)
+        torch.cuda.synchronize()
+        assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse), bad
