@@ -21,7 +21,8 @@
 // that BF16 values enter exactly unless they are 2^-30 below that; per-token
 // NVFP4 ones enter as dec(code) dec(block scale).  A unit's product starts
 // from zero and joins the row's sum under the running largest exponent, so
-// no sum overflows or underflows where the result does not.
+// no sum overflows where the result does not, nor loses more than 2^-149 of the
+// row's largest values' part.  The FP32 scales' exponents join that one.
 //
 // Split.  Of few weights (below MV_WHOLE_K_TILES tiles of 16 rows) a
 // workgroup's four wavefronts share K unit by unit and join through LDS for
@@ -99,6 +100,18 @@ __device__ __forceinline__ f16x8_t oct(uint32_t codes, _Float16 d)
     return f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
 }
 
+// The mantissa of an FP32 scale, in [1/2, 1); its exponent goes to e.
+__device__ __forceinline__ float mantissa(float scale, int *e)
+{
+    *e += __builtin_amdgcn_frexp_expf(scale);
+    return __builtin_amdgcn_frexp_mantf(scale);
+}
+// sum * scale * 2^e, in FP32's range where the result is.
+__device__ __forceinline__ float scaled(float sum, float scale, int e)
+{
+    const float v = sum * mantissa(scale, &e);
+    return __builtin_ldexpf(v, e);
+}
 // What a lane loads of an activation row's unit: 8 values.
 struct ActRaw {
     uint4 a, b;
@@ -516,10 +529,11 @@ __global__ void __launch_bounds__(64 * (WHOLE ? MV_MAX_WAVES : MV_SPLIT))
     const int lane = (int)lane_id(), wave = wave_in_group();
     auto src = [&](int r) { return (int64_t)m0 + r; };
     auto out = [&](int m, int64_t nn, const float *s, int e) {
-        float v = s[0] * a.scales[udiv((uint32_t)nn, a.per_scale)];
+        float v = s[0];
         if constexpr (FMT == MXQ_X_NVFP4)
-            v *= a.x.s[m0 + m];
-        st_elem<BF16_OUT>(a.c, (m0 + m) * a.N + nn, __builtin_ldexpf(v, e));
+            v *= mantissa(a.x.s[m0 + m], &e);
+        st_elem<BF16_OUT>(a.c, (m0 + m) * a.N + nn,
+                          scaled(v, a.scales[udiv((uint32_t)nn, a.per_scale)], e));
     };
     if constexpr (WHOLE) {
         const int t0 = wg * a.waves + wave;
@@ -603,10 +617,10 @@ __global__ void __launch_bounds__(64 * (WHOLE ? MV_MAX_WAVES : MV_SPLIT))
         auto out = [&](int m, int64_t nn, const float *s, int ee) {
             float sx = 1.0f;
             if constexpr (FMT == MXQ_X_NVFP4)
-                sx = a.x.s[src(m)];
-            float v = __builtin_ldexpf(s[0] * scale * sx, ee);
+                sx = mantissa(a.x.s[src(m)], &ee);
+            float v = scaled(s[0] * sx, scale, ee);
             if constexpr (GATED)
-                v = silu_f32(v) * __builtin_ldexpf(s[NW - 1] * scale * sx, ee);
+                v = silu_f32(v) * scaled(s[NW - 1] * sx, scale, ee);
             st_elem<BF16_OUT>(a.c, (c0 + m) * a.N + nn, v);
         };
         auto stage = [&] {

@@ -349,6 +349,50 @@ def test_experts_of_many_weights(G, rows, N, K, kind):
         close(h[a:z], silu * u, tol + 1e-36, f"gated pair of expert {e}")
 
 
+@pytest.mark.parametrize("kind", X_KINDS)
+@pytest.mark.parametrize("at", [-112, 112])
+@pytest.mark.parametrize("G,rows,N,K", [(3, 9, 40, 192), (128, 200, 257, 192)])
+def test_products_of_scales_far_apart(G, rows, N, K, at, kind):
+    """Activations about 2^at under weights about 2^-at: results about 1, whatever a part
+    of the product alone would be."""
+    announce(f"scales far apart {G} {rows}x{N}x{K} {kind} 2^{at}")
+    rng = np.random.default_rng(G + rows)
+    if kind == "nvfp4":
+        c, b, _ = R.random_nvfp4(rng, rows, K)
+        sx = np.exp2(at + rng.uniform(-12, -4, rows)).astype(np.float32)
+        x, xv, sx, held = api.NVFP4(dev(c), dev(b), dev(sx)), R.decode(c, b), sx.astype(np.float64), 0.0
+    else:
+        xv = bf16(rng.normal(0, 1, (rows, K)) * 2.0 ** at)
+        x = put(xv, torch.bfloat16 if kind == "bf16" else torch.float32)
+        sx, held = np.ones(rows), R.HALF_FP16 if kind == "f32" else 0.0
+    gc, gb, _ = R.random_nvfp4(rng, G * N, K)
+    s = np.exp2(-at + rng.uniform(-14, -9, G)).astype(np.float32)
+    seg = segments(rng, G, rows)
+    gd, gbd = (dev(a.reshape(G, N, -1)) for a in (gc, gb))
+    rt = np.arange(rows)
+    y = api.nvfp4_expert_matvec(x, gd, gbd, dev(s), dev(seg), torch.float32)
+    h = api.nvfp4_expert_gateup(x, api.GateUpNVFP4(gd, gbd, gd, gbd, dev(s)), dev(rt), dev(seg),
+                                torch.float32)
+    m = min(rows, 64)
+    few = (api.NVFP4(*(t[:m] for t in x)) if kind == "nvfp4" else x[:m])
+    e0 = int(np.argmax(np.diff(seg)))
+    dense = api.nvfp4_matvec(few, gd[e0], gbd[e0], dev(s[e0:e0 + 1].copy()), None, torch.float32)
+    torch.cuda.synchronize()
+    for e in range(G):
+        a, z = seg[e], seg[e + 1]
+        if z == a:
+            continue
+        w, sc = R.decode(gc[e * N:(e + 1) * N], gb[e * N:(e + 1) * N]), np.full(N, float(s[e]))
+        want, tol = product(xv[a:z], sx[a:z], w, sc, held)
+        close(y[a:z], want, tol, f"expert {e}")
+        with np.errstate(over="ignore"):
+            silu = want / (1 + np.exp(-want))
+        close(h[a:z], silu * want, 1.1 * tol * (np.abs(want) + tol) + np.abs(silu) * tol
+              + np.abs(silu * want) * 2.0 ** -20 + 1e-36, f"gated pair of expert {e}")
+        if e == e0:
+            close(dense, *product(xv[:m], sx[:m], w, sc, held), "dense")
+
+
 # ---------------------------------------------------------------------------
 # Attention over long walks and large batches
 # ---------------------------------------------------------------------------
