@@ -454,3 +454,97 @@ def test_attention_slots_before_the_window_hold_anything(lens, Q, H, Hkv, D, pag
         got = run_attention(*case, Hkv, page, None, True, window)
         torch.cuda.synchronize()
         assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse), bad
+
+
+# ---------------------------------------------------------------------------
+# Offsets past 32 bits: what a call uses stands at the end of large buffers,
+# whose other bytes hold anything
+# ---------------------------------------------------------------------------
+
+def at_the_end(t, rows):
+    """A tensor of `rows` rows that ends in t's."""
+    big = torch.empty((rows, *t.shape[1:]), dtype=t.dtype, device="cuda")
+    big[rows - t.shape[0]:] = t
+    return big
+
+
+def test_far_rows_of_the_router():
+    announce("far rows: router")
+    rng = np.random.default_rng(71)
+    x = put(bf16(rng.normal(0, 1.5, (70, 1024))), torch.bfloat16)
+    T = (1 << 22) + 70                                   # more than 2^32 logits
+    big = at_the_end(x, T)
+    want, got = (api.moe_route(t, 4, maps=False) for t in (x, big))
+    dw = put(rng.normal(0, 1, (70, 4)), torch.float32)
+    dx = api.moe_route_backward(dw, x, want.experts, renormalize=False)
+    dbig = api.moe_route_backward(at_the_end(dw, T), big, got.experts, renormalize=False)
+    torch.cuda.synchronize()
+    assert torch.equal(got.experts[-70:], want.experts)
+    assert torch.equal(got.weights[-70:], want.weights) and torch.equal(dbig[-70:], dx)
+
+
+def test_far_rows_of_the_combine():
+    announce("far rows: combine")
+    rng = np.random.default_rng(72)
+    T, k, cols, R_rows = 9, 3, 2056, (1 << 21) + 77      # more than 2^32 elements
+    rows = put(bf16(rng.normal(0, 1, (T * k, cols))), torch.bfloat16)
+    tr = torch.from_numpy(rng.permutation(T * k).reshape(T, k)).cuda()
+    w, d = put(rng.random((T, k)), torch.float32), put(bf16(rng.normal(0, 1, (T, cols))), torch.bfloat16)
+    big, far = at_the_end(rows, R_rows), tr + (R_rows - T * k)
+    out = [api.moe_combine(*a) for a in ((rows, tr, w), (big, far, w))]
+    back = [api.moe_combine_backward(d, *a) for a in ((rows, tr, w), (big, far, w))]
+    torch.cuda.synchronize()
+    assert torch.equal(*out) and torch.equal(back[0][1], back[1][1])
+    assert torch.equal(back[1][0][-T * k:], back[0][0])
+
+
+@pytest.mark.parametrize("N,K", [((1 << 24) - 5, 576)])
+def test_far_rows_of_a_dense_weight(N, K):
+    announce("far rows: dense weight")
+    rng = np.random.default_rng(73)
+    x, xv, sx, held = activation(rng, 5, K, "bf16")
+    c, b, _ = R.random_nvfp4(rng, 100, K)
+    s = torch.full((1,), 2.0 ** -8, device="cuda")
+    got = api.nvfp4_matvec(x, at_the_end(dev(c), N), at_the_end(dev(b), N), s, None, torch.float32)
+    torch.cuda.synchronize()
+    want, tol = product(xv, sx, R.decode(c, b), np.full(100, 2.0 ** -8), held)
+    close(got[:, -100:], want, tol, "dense")
+
+
+def test_far_rows_of_the_experts():
+    announce("far rows: experts")
+    rng = np.random.default_rng(74)
+    G, N, K, rows = 64, 32768, 4160, 7                   # 4.4 GB of codes
+    x, xv, sx, held = activation(rng, rows, K, "bf16")
+    c, b, _ = R.random_nvfp4(rng, 50, K)
+    s = torch.full((G,), 2.0 ** -8, device="cuda")
+    seg = torch.zeros(G + 1, dtype=torch.int64, device="cuda")
+    seg[-1] = rows
+    codes, blocks = (at_the_end(dev(a), G * N).view(G, N, -1) for a in (c, b))
+    y = api.nvfp4_expert_matvec(x, codes, blocks, s, seg)
+    h = api.nvfp4_expert_gateup(x, api.GateUpNVFP4(codes, blocks, codes, blocks, s),
+                                torch.arange(rows, device="cuda"), seg)
+    torch.cuda.synchronize()
+    want, tol = product(xv, sx, R.decode(c, b), np.full(50, 2.0 ** -8), held)
+    close(y[:, -50:], want, tol, "experts")
+    with np.errstate(over="ignore"):
+        silu = want / (1 + np.exp(-want))
+    close(h[:, -50:], silu * want, 1.1 * tol * (np.abs(want) + tol) + np.abs(silu) * tol
+          + np.abs(silu * want) * 2.0 ** -20 + 1e-36, "gated pair")
+
+
+@pytest.mark.parametrize("lens,Q,H,Hkv,D", [([700, 45], 1, 8, 2, 128), ([300, 201], 200, 16, 16, 64),
+                                            ([90], 3, 4, 2, 256)])
+def test_far_pages_of_a_cache(lens, Q, H, Hkv, D):
+    announce(f"far pages: attention D={D}")
+    rng = np.random.default_rng(75)
+    page = 32
+    q, k, v, table, lens = case = attention_case(rng, lens, Q, H, Hkv, D, page)
+    want = run_attention(*case, Hkv, page, None, True, 0)
+    near = k[0].shape[0]
+    rows = near + (1 << 33) // D // (Hkv * page) * (Hkv * page)      # 4.3 GB of codes before them
+    far = [api.NVFP4(*(at_the_end(dev(a), rows) for a in c)) for c in (k, v)]
+    got = api.nvfp4_attention(put(q, torch.bfloat16), *far, dev(table + (rows - near) // (Hkv * page)),
+                              dev(lens), Hkv, page)
+    torch.cuda.synchronize()
+    assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse)
