@@ -614,10 +614,13 @@ typedef struct {
  *   - weights[t][c] = scale s_c, with renormalize scale s_c / sum of the
  *     selected s.  The bias moves the selection only, not the weights.
  * The selection is that of the exact scores: where fp32 cannot decide, it is
- * decided in 64 bits.  Weights are fp32, within 2^-20 of their value.
- * An expert whose logit or bias is -inf (or NaN) is never selected; a logit
- * of +inf counts as the largest finite value.  Where fewer than top_k experts
- * are left, the other slots get expert -1, weight 0 and no row.
+ * decided in 64 bits.  Weights are fp32, within 2^-20 of their value, or
+ * scale 2^-126 where that is more.
+ * An expert whose logit or bias is -inf (or NaN) is never selected; with such
+ * a logit its score is 0, with such a bias it stays in the softmax's sum.  A
+ * logit of +inf counts as the largest finite fp32 value (above every finite
+ * BF16 logit).  Where fewer than top_k experts are left, the other slots get
+ * expert -1, weight 0 and no row.
  *
  *   logits       [n_tokens][n_experts] BF16 or fp32 (dtype: mxq_out_dtype),
  *                aligned to its element.
@@ -645,7 +648,8 @@ int64_t mxq_moe_route_workspace(int64_t n_tokens, int64_t n_experts);
  * Gradient of the router's weights: d_logits of L given d_weights = dL/dweights,
  * the selection held fixed (experts as mxq_moe_route returned them; an entry
  * outside [0, n_experts) contributes nothing).  Scores are recomputed from the
- * logits in fp32; d_logits has the logits' dtype, every entry written (0 for
+ * logits in fp32, renormalized ones from their ratios, in forms that keep fp32's
+ * relative precision where scores are near 0 or 1; d_logits has the logits' dtype, every entry written (0 for
  * an expert whose logit is -inf or NaN).
  *   top_k <= 64, other sizes as mxq_moe_route.
  */
@@ -774,9 +778,8 @@ typedef struct {
  *   block_table [n_seqs][max_pages] int64, seq_lens [n_seqs] int64, device data:
  *   lengths are clamped into [0, max_pages * page_size] and pages into
  *   [0, n_pages), so malformed ones give meaningless rows, never an access out
- *   of bounds; entries past a sequence's last page are not read.  Slots that
- *   no query sees (past the length, before the first query's window) may hold
- *   anything.
+ *   of bounds; entries past a sequence's last page may hold anything, and so may
+ *   slots that no query sees (past the length, before the first query's window).
  *   softmax_scale > 0; window >= 0, and 0 if not causal (MXQ_ERR_ARG).
  *   workspace: mxq_nvfp4_attention_workspace(...) bytes.
  *   n_seqs * q_len * n_heads <= 2^25, max_pages * page_size <= 2^30, cache rows
@@ -786,7 +789,7 @@ typedef struct {
  * softmax's numerators, times the values' FP32 scales, in FP16 (2^-11
  * relative) as far down as 2^-130 of the row's largest.  A value row whose FP32 scale is below
  * 2^-100 counts as zeros; the others of a sequence must lie within 2^100 of
- * each other.
+ * each other (and of 2^-8, if whole tiles of 32 keys may be zeros).
  */
 int mxq_nvfp4_attention(const uint16_t *q, const mxq_nvfp4_cache *k, const mxq_nvfp4_cache *v,
                         const int64_t *block_table, const int64_t *seq_lens, int64_t n_seqs,

@@ -555,7 +555,8 @@ def nvfp4_matvec(x, b_codes, b_block_scales, b_scales, rows_per_b_scale: Optiona
                  out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """C = x W^T for few rows x (at most 64): BF16 or FP32 [M][K], or an NVFP4
     tuple of per-token rows; W [N][K] in NVFP4 with one FP32 scale per
-    rows_per_b_scale rows (by default one for all).  Returns C [M][N]."""
+    rows_per_b_scale rows (by default one for all).  BF16 and NVFP4 activations
+    enter the products exactly, FP32 ones rounded to 11 bits.  Returns C [M][N]."""
     fmt, xv, xbs, xs, M, K = _activations(x)
     N = _nvfp4_weight(b_codes, b_block_scales, (), K, "b")
     rpb = N if rows_per_b_scale is None else rows_per_b_scale
@@ -611,7 +612,9 @@ def nvfp4_expert_layer(x, routing: Routing, gateup: GateUpNVFP4, down: GateUpNVF
     """The expert layer of a decode step: the routed experts' gate/up with
     SwiGLU, down, and the weighted return to the tokens.  x [T][K] BF16, FP32
     or NVFP4; gateup and down as nvfp4_quantize_gateup_pair exports them (down
-    with up=None).  Intermediates are FP32; returns BF16 [T][N]."""
+    with up=None).  Intermediates are FP32 tensors, of which the down product
+    holds its activations in FP16 under powers of two (as nvfp4_matvec); returns
+    BF16 [T][N]."""
     with _on(stream):
         h = nvfp4_expert_gateup(x, gateup, routing.row_tokens, routing.seg_offsets, stream=stream)
         y = nvfp4_expert_matvec(h, down.gate_codes, down.gate_block_scales, down.scope_scales,

@@ -19,7 +19,10 @@
 // Activations are staged once per workgroup in LDS as FP16, 128 values of a
 // row under one power of two (their largest magnitude in [2^14, 2^15)), so
 // that BF16 values enter exactly unless they are 2^-30 below that; per-token
-// NVFP4 ones enter as dec(code) dec(block scale).  A unit's product starts
+// NVFP4 ones enter as dec(code) dec(block scale).  FP32 ones are rounded to
+// FP16's 11 bits, three more than a BF16 result has: two FP16 parts of each
+// would take twice the LDS, so that a row of the largest K no longer fits,
+// and twice the matrix instructions.  A unit's product starts
 // from zero and joins the row's sum under the running largest exponent, so
 // no sum overflows where the result does not, nor loses more than 2^-149 of the
 // row's largest values' part.  The FP32 scales' exponents join that one.
@@ -30,7 +33,7 @@
 // tiles of its own and loads them in memory's order (see MvLine).  Either
 // way the next loads are issued before the current ones are multiplied.
 // Measured in graphs of ten calls: 1 x 2048 x 2048 4.7 us; 13 x 128257 x 2048
-// 36 us (151 MB: 4.2 TB/s); 1 x 1000000 x 2048 250 us (4.6 TB/s).
+// 35 us (151 MB: 4.3 TB/s); 1 x 1000000 x 2048 250 us (4.6 TB/s).
 #include <type_traits>
 
 #include "mxq_layer.h"
