@@ -21,8 +21,9 @@
 // that BF16 values enter exactly unless they are 2^-30 below that; per-token
 // NVFP4 ones enter as dec(code) dec(block scale).  FP32 ones are rounded to
 // FP16's 11 bits, three more than a BF16 result has: two FP16 parts of each
-// would take twice the LDS, so that a row of the largest K no longer fits,
-// and twice the matrix instructions.  A unit's product starts
+// (22 bits) take twice the LDS, so that a row of the largest K no longer fits,
+// and twice the matrix instructions (13 x 128256 x 2048 35 -> 46 us, 4 x 7168 x
+// 18432 67 -> 131 us, the experts of 48 tokens 85 -> 92 us).  A unit's product starts
 // from zero and joins the row's sum under the running largest exponent, so
 // no sum overflows where the result does not, nor loses more than 2^-149 of the
 // row's largest values' part.  The FP32 scales' exponents join that one.
