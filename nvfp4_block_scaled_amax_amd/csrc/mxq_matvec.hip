@@ -674,8 +674,8 @@ int whole_waves(int64_t rows, int units, int nw, int most)
 
 // Workgroups that the chip's 256 compute units hold with `lds` bytes each, at
 // most MV_CU_WAVES wavefronts a unit: a launch of about as many stages its
-// activations least often (32 x 8192 x 4096: 44 us with 512 workgroups,
-// 68 us with 1024).
+// activations least often (32 x 8192 x 4096 BF16: 30 us with 512 workgroups,
+// 37 us with 1024; 48 x 5120 x 2048: 17 and 23).
 int64_t resident_target(int64_t lds, int waves)
 {
     const int64_t per_cu = MV_LDS / lds, most = MV_CU_WAVES / waves;
