@@ -35,6 +35,17 @@ __device__ __forceinline__ float exp_f32(float x)
     return __builtin_fmaf(e, err * LN2, e);
 }
 
+// e^(x - m) for finite x and m.  The difference is rounded to half a step of it,
+// 2^-19 at 32 to 64, which the exponential would have as a relative error;
+// what it leaves (exact, by the two sums' errors) joins the result.
+__device__ __forceinline__ float exp_diff_f32(float x, float m)
+{
+    const float d = x - m, b = d - x;
+    const float lost = (x - (d - b)) - (m + b);
+    const float e = exp_f32(d);
+    return d > -120.0f ? __builtin_fmaf(e, lost, e) : e;     // below, d may be infinite
+}
+
 // x sigmoid(x), the sigmoid from the exponential that does not overflow.
 __device__ __forceinline__ float silu_f32(float x)
 {

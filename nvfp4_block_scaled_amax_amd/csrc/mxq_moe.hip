@@ -289,9 +289,8 @@ __device__ __forceinline__ float share_of(bool sigmoid, bool mine, float x)
     float h = over_lanes<L>(mine ? x : -__builtin_inff(), MaxOf{}), w = 0.0f;
     h = sigmoid && h > 0.0f ? 0.0f : h;
     if (mine)
-        w = !sigmoid ? exp_f32(x - h)
-            : x >= 0.0f ? 1.0f / (1.0f + exp_f32(-x))
-                        : exp_f32(x - h) / (1.0f + exp_f32(x));
+        w = sigmoid && x >= 0.0f ? 1.0f / (1.0f + exp_f32(-x))
+                                 : exp_diff_f32(x, h) / (sigmoid ? 1.0f + exp_f32(x) : 1.0f);
     const float s = over_lanes<L>(w, SumOf{});
     return s > 0.0f ? w / s : 0.0f;
 }
@@ -412,7 +411,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(RouteArgs a)
         if (a.renorm) {
             w = share_of<L>(a.sigmoid, mine, xv);
         } else if (mine) {
-            w = a.sigmoid ? 1.0f / (1.0f + exp_f32(-xv)) : exp_f32(xv - top) / den;
+            w = a.sigmoid ? 1.0f / (1.0f + exp_f32(-xv)) : exp_diff_f32(xv, top) / den;
         }
         if (live && l < a.top_k) {
             a.weights[t * a.top_k + l] = w * a.scale;
@@ -672,7 +671,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(Route
 #pragma unroll
             for (int j = 0; j < V; j++)
                 s[j] *= r;
-            q = ce >= 0 ? exp_f32(cx - m) * r : 0.0f;
+            q = ce >= 0 ? exp_diff_f32(cx, m) * r : 0.0f;
         }
         float u = 0.0f, gs = 0.0f, S = 0.0f;
         for (int c = 0; c < a.top_k; c++) {

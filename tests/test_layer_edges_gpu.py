@@ -108,6 +108,19 @@ def test_group_sums_of_keys_that_cancel(T, E, groups, at, scoring):
     check_route(x, b, params(6, scoring, groups, groups // 4, 2), torch.float32, "group sums")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("scoring", [mxq.MXQ_SCORE_SOFTMAX, mxq.MXQ_SCORE_SIGMOID])
+@pytest.mark.parametrize("T,E,k", [(200, 60, 30), (40, 640, 50), (3000, 16, 9)])
+def test_weights_of_logits_far_apart(T, E, k, scoring, renorm, dtype):
+    """Weights keep their 2^-20 where the logits differ by tens, a difference that FP32
+    rounds to 2^-19."""
+    rng = np.random.default_rng(T + E)
+    x = rng.normal(0, 14.0, (T, E))
+    x = bf16(x) if dtype == torch.bfloat16 else x.astype(np.float32).astype(np.float64)
+    check_route(x, None, params(k, scoring, renorm=renorm, scale=1.5), dtype, "far apart")
+
+
 # ---------------------------------------------------------------------------
 # Attention
 # ---------------------------------------------------------------------------
