@@ -787,9 +787,10 @@ typedef struct {
  * Scores, the running maximum and sum and the output are fp32; q is held in
  * FP16 under a power-of-two scale per row (as BF16 activations above) and the
  * softmax's numerators, times the values' FP32 scales, in FP16 (2^-11
- * relative) as far down as 2^-130 of the row's largest.  A value row whose FP32 scale is below
- * 2^-100 counts as zeros; the others of a sequence must lie within 2^100 of
- * each other (and of 2^-8, if whole tiles of 32 keys may be zeros).
+ * relative) as far down as 2^-100 of the row's largest.  A value row whose
+ * FP32 scale is below 2^-100 counts as zeros, under the largest scale of its 32
+ * keys or 2^-8; the others of a sequence must lie within 2^100 of each other
+ * (and of 2^-8, if whole tiles of 32 keys may be zeros).
  */
 int mxq_nvfp4_attention(const uint16_t *q, const mxq_nvfp4_cache *k, const mxq_nvfp4_cache *v,
                         const int64_t *block_table, const int64_t *seq_lens, int64_t n_seqs,
