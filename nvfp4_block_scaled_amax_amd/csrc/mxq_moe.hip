@@ -21,7 +21,7 @@
 // Many: a kernel between them forms those sums, one wavefront an expert.
 //
 // Bound by the selection's chain: 7 tokens x 256 experts in 8 groups take 9.0
-// us, 32768 x 128 top-8 14.6 us, then 5.8 us for the sums and 5.0 us for the maps.
+// us, 32768 x 128 top-8 14.7 us, then 6.3 us for the sums and 4.7 us for the maps.
 #include "mxq_layer.h"
 #include "mxq_layer_device.h"
 
